@@ -21,6 +21,7 @@ ERRORS = {
     -1: "FD_ERR_NULL_POINTER", -2: "FD_ERR_SHAPE", -3: "FD_ERR_GROUP", -4: "FD_ERR_HEAD_DIM",
     -5: "FD_ERR_ALIGNMENT", -6: "FD_ERR_WORKSPACE", -7: "FD_ERR_SPLITS", -8: "FD_ERR_DEVICE",
     -9: "FD_ERR_LAUNCH", -10: "FD_ERR_TIMEOUT", -11: "FD_ERR_CAPACITY", -12: "FD_ERR_STATIC_LIMIT", -13: "FD_ERR_BOUNDS",
+    -14: "FD_ERR_OVERLAP",
 }
 FD_STATIC_SCRATCH_BYTES = 8 << 20
 FD_KV_HND, FD_KV_NHD = 0, 1
@@ -35,6 +36,7 @@ class FdError(RuntimeError):
 
 _lib = None
 _i, _p, _sz, _f = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+_ll = ctypes.c_longlong
 
 
 def _newer_sources(path: str) -> list:
@@ -78,12 +80,22 @@ def lib() -> ctypes.CDLL:
         L.fd_merge_partials.argtypes = [_i, _i, _i, _p, _p, _p, _p, _p]
         L.fd_read_probe.argtypes = [_p, _sz, _p, _p]
         L.fd_decode_quant_paged.argtypes = [_i] * 10 + [_p] * 7 + [_f, _p, _p, _p, _sz, _i, _p]
+        L.fd_decode_quant_block.argtypes = [_i] * 8 + [_p] * 6 + [_f, _p, _p, _p, _sz, _i, _p]
+        L.fd_decode_quant_block_paged.argtypes = [_i] * 11 + [_p] * 7 + [_f, _p, _p, _p, _sz, _i, _p]
+        L.fd_quant_append.argtypes = [_i] * 7 + [_p, _p, _ll, _ll, _ll] + [_p] * 7
+        L.fd_quant_append_paged.argtypes = [_i] * 10 + [_p, _p, _ll, _ll, _ll] + [_p] * 8
+        L.fd_weights_workspace_bytes.argtypes = [_i] * 7
+        L.fd_weights_workspace_bytes.restype = _sz
+        L.fd_decode_weights.argtypes = [_i] * 6 + [_p, _p, _p, _p, _f] + [_p] * 5 + [_sz, _i, _p]
+        L.fd_evict.argtypes = [_i] * 7 + [_p] * 10
         L.fd_strerror.argtypes = [_i]
         L.fd_strerror.restype = ctypes.c_char_p
         L.fd_version.argtypes = []
         for name in ("fd_plan", "fd_plan_for_sms", "fd_decode", "fd_decode_splits", "fd_split", "fd_combine",
                      "fd_segments", "fd_device_status", "fd_version", "fd_workspace_init", "fd_decode_static",
-                     "fd_decode_paged", "fd_decode_multi", "fd_decode_quant", "fd_merge_partials", "fd_read_probe", "fd_decode_quant_paged"):
+                     "fd_decode_paged", "fd_decode_multi", "fd_decode_quant", "fd_merge_partials", "fd_read_probe", "fd_decode_quant_paged",
+                     "fd_decode_quant_block", "fd_decode_quant_block_paged", "fd_quant_append", "fd_quant_append_paged",
+                     "fd_decode_weights", "fd_evict"):
             getattr(L, name).restype = _i
         _lib = L
     return _lib
@@ -550,3 +562,381 @@ def decode(q, k_cache, v_cache, seqlens, scale, num_splits=None, stream=None):
     lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     fd_decode_splits(q, k_cache, v_cache, seqlens, scale, out, lse, ws, S, stream)
     return out, lse
+
+
+# -------------------------------------------------------- cache compression --
+# 8-bit caches with one scale per block of tokens (append and attention),
+# attention weights per cached token, eviction by them (see include/fd.h).
+
+FD_BLOCK_TOKENS = (16, 32, 64, 128)
+
+
+def _tensor(t, name, shape, dtype):
+    if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {list(shape)}")
+
+
+def _one_device(*tensors):
+    """Index of the device that holds all of `tensors` (None entries aside)."""
+    devices = {t.device.index for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("all tensors must be on one device")
+    return devices.pop()
+
+
+def _prepared(what, device, args):
+    """A no-argument callable that runs entry point `what` with `args`, with
+    `device` (where the tensors are) as the current device."""
+    fn = getattr(lib(), what)
+    # converted once here, not on every call
+    args = tuple(t(a) if a is not None else a for t, a in zip(fn.argtypes, args))
+
+    def call():
+        if torch.cuda.current_device() == device:
+            rc = fn(*args)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args)
+        if rc != 0:
+            raise FdError(rc, what)
+
+    return call
+
+
+def _planned(device, B, Hq, Hkv, D, Lmax, num_splits):
+    if num_splits is not None:
+        return int(num_splits)
+    with torch.cuda.device(device):
+        return fd_plan(B, Hq, Hkv, D, Lmax)
+
+
+def _query(q):
+    if q.dim() not in (3, 4) or q.dtype != torch.bfloat16 or not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 CUDA tensor [B, Hq, D] or [B, q_len, Hq, D]")
+    return q.shape[0], 1 if q.dim() == 3 else q.shape[1], q.shape[-2], q.shape[-1]
+
+
+def _block_codes(k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens):
+    """(B, Hkv, Lmax, D) of a contiguous block-scaled cache."""
+    if kv_type not in KV_CODES:
+        raise ValueError("kv_type must be 'e4m3' or 'int8'")
+    if block_tokens not in FD_BLOCK_TOKENS:
+        raise ValueError(f"block_tokens must be one of {FD_BLOCK_TOKENS}")
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes, v_codes must be [B, Hkv, Lmax, D]")
+    B, Hkv, Lmax, D = k_codes.shape
+    for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+        _tensor(t, name, k_codes.shape, torch.uint8)
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _tensor(t, name, (B, Hkv, -(-Lmax // block_tokens)), torch.float32)
+    return B, Hkv, Lmax, D
+
+
+def _block_pages(k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, layout):
+    """(Hkv, D, page_size, num_pages, max_pages) of a paged block-scaled cache."""
+    if kv_type not in KV_CODES:
+        raise ValueError("kv_type must be 'e4m3' or 'int8'")
+    if layout not in LAYOUTS:
+        raise ValueError("layout must be 'HND' ([pages, Hkv, page_size, D]) or 'NHD' ([pages, page_size, Hkv, D])")
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("expected k_pages, v_pages 4-D and block_table [B, max_pages]")
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _tensor(t, name, k_pages.shape, torch.uint8)
+    num_pages, page_size, D = k_pages.shape[0], k_pages.shape[2 if layout == "HND" else 1], k_pages.shape[3]
+    Hkv = k_pages.shape[1 if layout == "HND" else 2]
+    if block_tokens not in FD_BLOCK_TOKENS or block_tokens > page_size:
+        raise ValueError(f"block_tokens must be one of {FD_BLOCK_TOKENS} and at most the page size")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _tensor(t, name, (num_pages, Hkv, page_size // block_tokens), torch.float32)
+    _tensor(block_table, "block_table", block_table.shape, torch.int32)
+    return Hkv, D, page_size, num_pages, block_table.shape[1]
+
+
+def _block_outputs(q, out, lse):
+    _tensor(out, "out", q.shape, torch.float32)
+    _tensor(lse, "lse", q.shape[:-1], torch.float32)
+
+
+def prepare_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse,
+                               workspace=None, num_splits=None, stream=None):
+    """Check and marshal once; return a no-argument callable that enqueues
+    fd_decode_quant_block with those pointers on `stream` (None: the stream
+    current now): attention over uint8 codes [B, Hkv, Lmax, D] with float32
+    scales [B, Hkv, ceil(Lmax / block_tokens)]; q [B, Hq, D] or
+    [B, q_len, Hq, D], out / lse shaped to match; workspace as for
+    fd_decode_quant (quant_workspace_bytes)."""
+    B, Hkv, Lmax, D = _block_codes(k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens)
+    Bq, q_len, Hq, Dq = _query(q)
+    if Bq != B or Dq != D:
+        raise ValueError("q and the cache disagree on B or D")
+    _block_outputs(q, out, lse)
+    _seqlens(seqlens, B)
+    wp, wb = _ws(workspace)
+    dev = _one_device(q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, workspace)
+    S = _planned(dev, B, Hq, Hkv, D, Lmax, num_splits)
+    call = _prepared("fd_decode_quant_block", dev, (
+        B, q_len, Hq, Hkv, D, Lmax, block_tokens, KV_CODES[kv_type], q.data_ptr(), k_codes.data_ptr(),
+        v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(),
+        lse.data_ptr(), wp, wb, S, _stream(stream, q.device)))
+    call.num_splits = S
+    return call
+
+
+def fd_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse,
+                          workspace=None, num_splits=0, stream=None):
+    """prepare_decode_quant_block, enqueued once; num_splits 0 lets the library
+    plan the split count."""
+    prepare_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse,
+                               workspace, num_splits, stream)()
+
+
+def decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, num_splits=None,
+                       stream=None):
+    """Allocate out / lse / workspace with torch and run fd_decode_quant_block."""
+    _, Hkv, Lmax, _ = _block_codes(k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens)
+    B, _, Hq, D = _query(q)
+    S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
+    nbytes = quant_workspace_bytes(q, k_codes, S)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fd_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse, ws, S,
+                          stream)
+    return out, lse
+
+
+def prepare_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
+                                     scale, out, lse, workspace=None, layout="HND", num_splits=None, stream=None):
+    """prepare_decode_quant_block over page pools: codes as for
+    fd_decode_quant_paged, scales [num_pages, Hkv, page_size / block_tokens]."""
+    Hkv, D, page_size, num_pages, max_pages = _block_pages(k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens,
+                                                           block_table, layout)
+    B, q_len, Hq, Dq = _query(q)
+    if Dq != D or block_table.shape[0] != B:
+        raise ValueError("q, pages and block_table disagree on B or D")
+    _block_outputs(q, out, lse)
+    _seqlens(seqlens, B)
+    wp, wb = _ws(workspace)
+    dev = _one_device(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
+    S = _planned(dev, B, Hq, Hkv, D, max_pages * page_size, num_splits)
+    call = _prepared("fd_decode_quant_block_paged", dev, (
+        B, q_len, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], block_tokens, KV_CODES[kv_type],
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, S,
+        _stream(stream, q.device)))
+    call.num_splits = S
+    return call
+
+
+def fd_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
+                                scale, out, lse, workspace=None, layout="HND", num_splits=0, stream=None):
+    """prepare_decode_quant_block_paged, enqueued once."""
+    prepare_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
+                                     scale, out, lse, workspace, layout, num_splits, stream)()
+
+
+def decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens, scale,
+                             layout="HND", num_splits=None, stream=None):
+    """Allocate out / lse / workspace with torch and run
+    fd_decode_quant_block_paged."""
+    Hkv, D, page_size, _, max_pages = _block_pages(k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens,
+                                                   block_table, layout)
+    B, q_len, Hq, _ = _query(q)
+    Lmax = max_pages * page_size
+    S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
+    nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    fd_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens, scale,
+                                out, lse, ws, layout, S, stream)
+    return out, lse
+
+
+def _new_tokens(k_new, v_new, B, Hkv, D):
+    """n_new and the element strides of k_new / v_new [B, n_new, Hkv, D] (any
+    strides that are multiples of 8, head dim contiguous)."""
+    if k_new.dim() != 4 or v_new.shape != k_new.shape or k_new.shape[0] != B or k_new.shape[2:] != (Hkv, D):
+        raise ValueError("k_new, v_new must be [B, n_new, Hkv, D]")
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a bf16 CUDA tensor with a contiguous head dimension")
+    # the stride of a dimension of length 1 says nothing
+    strides = [[0 if t.shape[d] == 1 else t.stride(d) for d in range(3)] for t in (k_new, v_new)]
+    if strides[0] != strides[1]:
+        raise ValueError("k_new and v_new must have the same strides")
+    return k_new.shape[1], strides[0]
+
+
+def _append_lens(new_lens, seqlens, B):
+    _seqlens(seqlens, B)
+    if not seqlens.is_contiguous():
+        raise ValueError("seqlens must be contiguous")
+    if new_lens is None:
+        return None
+    _tensor(new_lens, "new_lens", (B,), torch.int32)
+    return new_lens.data_ptr()
+
+
+def prepare_quant_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, new_lens=None,
+                         stream=None):
+    """Check and marshal once; return a no-argument callable that enqueues
+    fd_quant_append with those pointers: bf16 tokens k_new, v_new
+    [B, n_new, Hkv, D] (a view with any strides that are multiples of 8, e.g.
+    a transposed [B, Hkv, n_new, D] cache) into a block-scaled cache (see
+    prepare_decode_quant_block). seqlens counts the new tokens; new_lens
+    [B] int32 gives how many of the n_new each sequence has (None: all)."""
+    B, Hkv, Lmax, D = _block_codes(k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens)
+    n_new, (sb, st, sh) = _new_tokens(k_new, v_new, B, Hkv, D)
+    lens = _append_lens(new_lens, seqlens, B)
+    dev = _one_device(k_new, v_new, k_codes, v_codes, k_scale, v_scale, seqlens, new_lens)
+    return _prepared("fd_quant_append", dev, (
+        B, n_new, Hkv, D, Lmax, block_tokens, KV_CODES[kv_type], k_new.data_ptr(), v_new.data_ptr(), sb, st, sh, lens,
+        seqlens.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        _stream(stream, k_new.device)))
+
+
+def fd_quant_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, new_lens=None,
+                    stream=None):
+    """prepare_quant_append, enqueued once."""
+    prepare_quant_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, new_lens,
+                         stream)()
+
+
+def prepare_quant_append_paged(k_new, v_new, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table,
+                               seqlens, new_lens=None, layout="HND", stream=None):
+    """prepare_quant_append into page pools (see
+    prepare_decode_quant_block_paged)."""
+    Hkv, D, page_size, num_pages, max_pages = _block_pages(k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens,
+                                                           block_table, layout)
+    B = block_table.shape[0]
+    n_new, (sb, st, sh) = _new_tokens(k_new, v_new, B, Hkv, D)
+    lens = _append_lens(new_lens, seqlens, B)
+    dev = _one_device(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, new_lens)
+    return _prepared("fd_quant_append_paged", dev, (
+        B, n_new, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], block_tokens, KV_CODES[kv_type],
+        k_new.data_ptr(), v_new.data_ptr(), sb, st, sh, lens, block_table.data_ptr(), seqlens.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _stream(stream, k_new.device)))
+
+
+def fd_quant_append_paged(k_new, v_new, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
+                          new_lens=None, layout="HND", stream=None):
+    """prepare_quant_append_paged, enqueued once."""
+    prepare_quant_append_paged(k_new, v_new, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table,
+                               seqlens, new_lens, layout, stream)()
+
+
+def empty_quant_block_cache(B, Hkv, max_len, D, block_tokens, device="cuda"):
+    """Codes and scales of an empty contiguous block-scaled cache, zeroed:
+    k_codes, v_codes, k_scale, v_scale, for fd_quant_append to fill."""
+    if block_tokens not in FD_BLOCK_TOKENS:
+        raise ValueError(f"block_tokens must be one of {FD_BLOCK_TOKENS}")
+    blocks = -(-max_len // block_tokens)
+    codes = [torch.zeros((B, Hkv, max_len, D), dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.zeros((B, Hkv, blocks), dtype=torch.float32, device=device) for _ in range(2)]
+    return codes[0], codes[1], scales[0], scales[1]
+
+
+def fd_weights_workspace_bytes(B: int, q_len: int, Hq: int, Hkv: int, D: int, max_len: int, num_splits: int) -> int:
+    return int(lib().fd_weights_workspace_bytes(B, q_len, Hq, Hkv, D, max_len, num_splits))
+
+
+def prepare_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights_in, weights_out, workspace,
+                           num_splits=None, stream=None):
+    """Check and marshal once; return a no-argument callable that enqueues
+    fd_decode_weights with those pointers: decode attention (q [B, Hq, D] or
+    [B, q_len, Hq, D]) that also writes weights_out [B, Hkv, Lmax] =
+    weights_in (None: zeros; may be weights_out) + each cached token's
+    attention weight. workspace: fd_weights_workspace_bytes, zeroed once."""
+    B, q_len, Hq, D = _query(q)
+    _, _, Hkv, _, Lmax = _shapes(q.view(B, q_len * Hq, D), k_cache, v_cache)
+    _block_outputs(q, out, lse)
+    _seqlens(seqlens, B)
+    for t, name in ((weights_in, "weights_in"), (weights_out, "weights_out")):
+        if t is not None or name == "weights_out":
+            _tensor(t, name, (B, Hkv, Lmax), torch.float32)
+    wp, wb = _ws(workspace)
+    dev = _one_device(q, k_cache, v_cache, seqlens, out, lse, weights_in, weights_out, workspace)
+    S = _planned(dev, B, Hq, Hkv, D, Lmax, num_splits)
+    call = _prepared("fd_decode_weights", dev, (
+        B, q_len, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
+        float(scale), out.data_ptr(), lse.data_ptr(), None if weights_in is None else weights_in.data_ptr(),
+        weights_out.data_ptr(), wp, wb, S, _stream(stream, q.device)))
+    call.num_splits = S
+    return call
+
+
+def fd_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights_in, weights_out, workspace, num_splits=0,
+                      stream=None):
+    """prepare_decode_weights, enqueued once; num_splits 0 lets the library
+    plan the split count."""
+    prepare_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights_in, weights_out, workspace, num_splits,
+                           stream)()
+
+
+def decode_weights(q, k_cache, v_cache, seqlens, scale, weights=None, num_splits=None, stream=None):
+    """Allocate out / lse / workspace with torch and run fd_decode_weights.
+    `weights` [B, Hkv, Lmax] is updated in place (None: a new one, from zeros).
+    Returns (out, lse, weights)."""
+    B, q_len, Hq, D = _query(q)
+    _, _, Hkv, _, Lmax = _shapes(q.view(B, q_len * Hq, D), k_cache, v_cache)
+    S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
+    nbytes = fd_weights_workspace_bytes(B, q_len, Hq, Hkv, D, Lmax, S)
+    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    if weights is None:
+        weights = torch.zeros((B, Hkv, Lmax), dtype=torch.float32, device=q.device)
+    fd_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights, weights, ws, S, stream)
+    return out, lse, weights
+
+
+def prepare_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, weights_out, kept, seqlens_out,
+                  stream=None):
+    """Check and marshal once; return a no-argument callable that enqueues
+    fd_evict with those pointers: caches [B, Hkv, Lmax, D] bf16 and totals
+    `weights` [B, Hkv, Lmax] cut to `keep` tokens per (sequence, kv head), the
+    last `recent` and the heaviest others, into k_out, v_out
+    [B, Hkv, out_len, D], weights_out [B, Hkv, out_len], kept [B, Hkv, keep]
+    int32 and seqlens_out [B] int32."""
+    if k_cache.dim() != 4 or k_out.dim() != 4:
+        raise ValueError("k_cache and k_out must be [B, Hkv, length, D]")
+    B, Hkv, Lmax, D = k_cache.shape
+    out_len = k_out.shape[2]
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _tensor(t, name, k_cache.shape, torch.bfloat16)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _tensor(t, name, (B, Hkv, out_len, D), torch.bfloat16)
+    _tensor(weights, "weights", (B, Hkv, Lmax), torch.float32)
+    _tensor(weights_out, "weights_out", (B, Hkv, out_len), torch.float32)
+    _tensor(kept, "kept", (B, Hkv, keep), torch.int32)
+    for t, name in ((seqlens, "seqlens"), (seqlens_out, "seqlens_out")):
+        _tensor(t, name, (B,), torch.int32)
+    dev = _one_device(k_cache, v_cache, weights, seqlens, k_out, v_out, weights_out, kept, seqlens_out)
+    return _prepared("fd_evict", dev, (
+        B, Hkv, D, Lmax, keep, recent, out_len, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
+        seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), kept.data_ptr(),
+        seqlens_out.data_ptr(), _stream(stream, k_cache.device)))
+
+
+def fd_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, weights_out, kept, seqlens_out,
+             stream=None):
+    """prepare_evict, enqueued once."""
+    prepare_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, weights_out, kept, seqlens_out,
+                  stream)()
+
+
+def evict(k_cache, v_cache, weights, seqlens, keep, recent=0, out_len=None, stream=None):
+    """Allocate the outputs with torch and run fd_evict; out_len (default
+    keep) tokens are allocated per row, so a decode loop can append to the cut
+    cache. Returns (k_out, v_out, weights_out, kept, seqlens_out)."""
+    B, Hkv, _, D = k_cache.shape
+    n = keep if out_len is None else int(out_len)
+    dev = k_cache.device
+    k_out = torch.zeros((B, Hkv, n, D), dtype=torch.bfloat16, device=dev)
+    v_out = torch.zeros_like(k_out)
+    w_out = torch.empty((B, Hkv, n), dtype=torch.float32, device=dev)
+    kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+    lens = torch.empty((B,), dtype=torch.int32, device=dev)
+    fd_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, w_out, kept, lens, stream)
+    return k_out, v_out, w_out, kept, lens

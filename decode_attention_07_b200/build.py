@@ -2,6 +2,8 @@
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -10,14 +12,15 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(PKG, "libfdecode.so")
 DEBUG_LIBRARY = os.path.join(PKG, "libfdecode_debug.so")   # -DFD_DEBUG: device-side bounds checks
 HOST_BENCH = os.path.join(PKG, "fd_host_bench")   # host time per call through the C ABI (bench.py runs it)
-SOURCES = [os.path.join(CSRC, "fd_api.cu"), os.path.join(CSRC, "fd_probe.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fd_api.cu", "fd_block.cu", "fd_weights.cu", "fd_append.cu", "fd_evict.cu",
+                                           "fd_probe.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + \
     [os.path.join(INCLUDE, "fd.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-std=c++17", "-lineinfo",
-    "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "-cudart", "static",
 ]
 
@@ -53,10 +56,14 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str = None, deb
     out = out or (DEBUG_LIBRARY if debug else LIBRARY)
     if not force and up_to_date(out):
         return out
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-DFD_DEBUG"] if debug else []), "-I", INCLUDE, "-I", CSRC, "-o", out, *SOURCES]
-    if verbose_ptxas:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    subprocess.run(cmd, check=True)
+    cc = [nvcc(), *NVCC_FLAGS, *(["-DFD_DEBUG"] if debug else []), *(["-Xptxas", "-v"] if verbose_ptxas else []),
+          "-I", INCLUDE, "-I", CSRC]
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, os.path.basename(src) + ".o") for src in SOURCES]
+        with ThreadPoolExecutor(os.cpu_count() or 1) as pool:   # one compiler per source
+            list(pool.map(lambda so: subprocess.run([*cc, "-c", "-o", so[1], so[0]], check=True),
+                          zip(SOURCES, objects)))
+        subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", "-o", out, *objects], check=True)
     return out
 
 

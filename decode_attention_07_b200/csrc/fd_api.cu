@@ -11,20 +11,17 @@
 
 #include "fd.h"
 #include "fd_combine.cuh"
+#include "fd_host.cuh"
 #include "fd_partials.cuh"
 #include "fd_partition.cuh"
 #include "fd_quant.cuh"
 #include "fd_split.cuh"
 
-namespace {
+namespace fdh {
 
 constexpr int kVersion = 100;               // 0.1.0
 constexpr int kMinTilesPerSplit = 4;        // a split streams at least 256 tokens per kv head
 constexpr int kMidTilesPerSm = 16;          // up to this many tiles per SM, splits come in multiples of 32
-constexpr int kMaxDevices = 64;
-constexpr float kLog2e = 1.4426950408889634f;
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // ----------------------------------------------------------- shape checks --
 int check_shape(int B, int Hq, int Hkv, int D, int max_len) {
@@ -44,13 +41,6 @@ long long num_slots(int B, int Hkv, int num_splits) {
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Workspace: seg_out [slots][g][D] fp32 | seg_lse [slots][g] fp32 | row tickets [B*Hkv] int32
-// followed by chunk tickets [slots] int32,
-// each part 256-byte aligned.
-struct WorkspaceLayout {
-    size_t seg_out, seg_lse, tickets, total;
-};
 
 WorkspaceLayout workspace_layout(int B, int Hq, int Hkv, int D, int num_splits) {
     WorkspaceLayout w{0, 0, 0, 0};
@@ -197,7 +187,7 @@ int encode_tiled(CUtensorMap *map, CUtensorMapDataType dtype, int rank, const vo
 // box = 64 head-dim elements (128 bytes, 128-byte swizzle) x 64 tokens x 1
 // row. 8-bit codes (one_byte): box = all D codes of a token (128 bytes with
 // the 128-byte swizzle for D = 128, 64 bytes with the 64-byte one for D = 64).
-int encode_cache_map(CUtensorMap *map, const void *base, int D, int Lmax, long long rows, bool one_byte = false) {
+int encode_cache_map(CUtensorMap *map, const void *base, int D, int Lmax, long long rows, bool one_byte) {
     const cuuint64_t e = one_byte ? 1 : 2;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Lmax), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * e, static_cast<cuuint64_t>(Lmax) * D * e};
@@ -228,7 +218,7 @@ int encode_cache_map_rows(CUtensorMap *map, const void *base, int Lmax, long lon
 // tensor either way (TMA fills zeros). 8-bit codes (one_byte): boxes of all D
 // codes of a token (64-byte swizzle for D = 64).
 int encode_paged_map(CUtensorMap *map, const void *base, int D, int page_size, int Hkv, long long num_pages,
-                     bool nhd, bool one_byte = false) {
+                     bool nhd, bool one_byte) {
     const cuuint64_t e = one_byte ? 1 : 2;   // 8-bit codes or bf16
     const cuuint32_t rows = static_cast<cuuint32_t>(page_size < fd::kTileTokens ? page_size : fd::kTileTokens);
     const cuuint64_t row = static_cast<cuuint64_t>(D) * e;   // bytes of one token of one head
@@ -357,48 +347,6 @@ int debug_spoil_guess() {
 }
 
 // ---------------------------------------------------------------- launches --
-template <int D, class Consumer, bool kFused, bool kPaged>
-int launch_split_t(const CUtensorMap &tk, const CUtensorMap &tv, const fd::SplitParams &p, cudaStream_t st,
-                   const CUtensorMap *rk = nullptr, const CUtensorMap *rv = nullptr) {
-    constexpr int smem = fd::SplitConfig<D, Consumer::G, Consumer::kElemBytes, kPaged>::kSmemBytes;
-    auto kern = fd::fd_split_kernel<D, Consumer, kFused, kPaged>;
-    // the attribute is per function and device; set it once per device
-    static std::once_flag once[kMaxDevices];
-    static cudaError_t attr_err[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        cudaGetLastError();
-        return FD_ERR_DEVICE;
-    }
-    std::call_once(once[dev], [&] {
-        attr_err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    });
-    if (attr_err[dev] != cudaSuccess) {
-        cudaGetLastError();
-        return FD_ERR_LAUNCH;
-    }
-    // programmatic dependent launch: the prologue overlaps the previous
-    // kernel's tail; the kernel waits for it before reading any input
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>(p.P));
-    cfg.blockDim = dim3(fd::split_threads<kPaged>());
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (inject_launch_failure()) return FD_ERR_LAUNCH;
-    // the maps of consecutive page runs (small pages only; never read otherwise)
-    if (cudaLaunchKernelEx(&cfg, kern, tk, tv, rk ? *rk : tk, rv ? *rv : tv, p) != cudaSuccess) {
-        cudaGetLastError();
-        return FD_ERR_LAUNCH;
-    }
-    return FD_OK;
-}
-
 template <bool kFused, bool kPaged = false>
 int launch_split(int D, int g, const CUtensorMap &tk, const CUtensorMap &tv, const fd::SplitParams &p,
                  cudaStream_t st, const CUtensorMap *rk = nullptr, const CUtensorMap *rv = nullptr) {
@@ -449,18 +397,6 @@ int launch_combine(int D, const fd::CombineParams &p, cudaStream_t st, bool afte
     return FD_OK;
 }
 
-struct Problem {
-    int B, Hq, Hkv, D, max_len;
-    const uint16_t *q, *k, *v;
-    const int32_t *seqlens;
-    float scale;
-    float *out, *lse;
-    void *ws;
-    size_t ws_bytes;
-    int num_splits;
-    cudaStream_t stream;
-};
-
 // Checks shared by every compute entry point (no CUDA call).
 int check_problem(const Problem &pr, bool need_kv) {
     int rc = check_shape(pr.B, pr.Hq, pr.Hkv, pr.D, pr.max_len);
@@ -483,7 +419,7 @@ int check_problem(const Problem &pr, bool need_kv) {
 }
 
 // `q_len` query positions per sequence: a segment holds q_len * g columns.
-void seg_pointers(const Problem &pr, float **so, float **sl, int **tickets, int q_len = 1) {
+void seg_pointers(const Problem &pr, float **so, float **sl, int **tickets, int q_len) {
     const WorkspaceLayout w = workspace_layout(pr.B, pr.Hq * q_len, pr.Hkv, pr.D, pr.num_splits);
     if (w.total == 0) {
         *so = *sl = nullptr;
@@ -494,6 +430,47 @@ void seg_pointers(const Problem &pr, float **so, float **sl, int **tickets, int 
     *so = reinterpret_cast<float *>(base + w.seg_out);
     *sl = reinterpret_cast<float *>(base + w.seg_lse);
     *tickets = reinterpret_cast<int *>(base + w.tickets);
+}
+
+int check_paged(int page_size, int num_pages, int max_pages_per_seq, int kv_layout, long long *max_len) {
+    if (page_size < 8 || page_size > 4096 || (page_size & (page_size - 1)) != 0) return FD_ERR_SHAPE;
+    if (num_pages < 1 || max_pages_per_seq < 1 || (max_pages_per_seq % 4) != 0) return FD_ERR_SHAPE;
+    if (kv_layout != FD_KV_HND && kv_layout != FD_KV_NHD) return FD_ERR_SHAPE;
+    *max_len = static_cast<long long>(max_pages_per_seq) * page_size;
+    return *max_len > 0x7fffffffLL ? FD_ERR_SHAPE : FD_OK;
+}
+
+fd::SplitParams split_params(const Problem &pr, int q_len, const PagedLayout *pl) {
+    fd::SplitParams p;
+    std::memset(&p, 0, sizeof p);
+    p.q = pr.q;
+    p.seqlens = pr.seqlens;
+    p.out = pr.out;
+    p.lse = pr.lse;
+    seg_pointers(pr, &p.seg_out, &p.seg_lse, &p.row_tickets, q_len);
+    p.chunk_tickets = p.row_tickets ? p.row_tickets + static_cast<size_t>(pr.B) * pr.Hkv : nullptr;
+    p.B = pr.B;
+    p.Hq = pr.Hq;
+    p.Hkv = pr.Hkv;
+    p.g = pr.Hq / pr.Hkv;
+    p.Lmax = pr.max_len;
+    p.P = pr.num_splits;
+    p.q_len = q_len;
+    p.cols = p.g * q_len;
+    p.scale_log2e = pr.scale * kLog2e;
+    if (pl != nullptr) {
+        p.block_table = pl->block_table;
+        p.max_pages = pl->max_pages;
+        while ((1 << p.page_shift) < pl->page_size) ++p.page_shift;
+        p.kv_nhd = pl->nhd ? 1 : 0;
+        p.num_pages = pl->num_pages;
+    } else {
+        p.k_base = pr.k;
+        p.v_base = pr.v;
+    }
+    p.debug_withhold = debug_withhold();
+    p.debug_spoil_guess = debug_spoil_guess();
+    return p;
 }
 
 // The split kernel; `fused` adds the in-kernel combine (fd_decode), without it
@@ -520,32 +497,7 @@ int run_split(const Problem &pr, bool fused, int q_len = 1) {
     } else if (!fused) {
         return FD_OK;   // no tokens anywhere: the combine writes every row
     }
-    fd::SplitParams p;
-    p.q = pr.q;
-    p.seqlens = pr.seqlens;
-    p.out = pr.out;
-    p.lse = pr.lse;
-    seg_pointers(pr, &p.seg_out, &p.seg_lse, &p.row_tickets, q_len);
-    p.chunk_tickets = p.row_tickets ? p.row_tickets + static_cast<size_t>(pr.B) * pr.Hkv : nullptr;
-    p.B = pr.B;
-    p.Hq = pr.Hq;
-    p.Hkv = pr.Hkv;
-    p.g = pr.Hq / pr.Hkv;
-    p.Lmax = pr.max_len;
-    p.P = pr.num_splits;
-    p.q_len = q_len;
-    p.cols = p.g * q_len;
-    p.scale_log2e = pr.scale * kLog2e;
-    p.block_table = nullptr;
-    p.max_pages = 0;
-    p.page_shift = 0;
-    p.kv_nhd = 0;
-    p.num_pages = 0;
-    p.k_scale = p.v_scale = nullptr;
-    p.k_base = pr.k;
-    p.v_base = pr.v;
-    p.debug_withhold = debug_withhold();
-    p.debug_spoil_guess = debug_spoil_guess();
+    const fd::SplitParams p = split_params(pr, q_len, nullptr);
     // with max_len == 0 every block finds zero tiles and only writes empty rows;
     // the (unused) tensor maps stay zeroed
     if (rows_map)
@@ -554,12 +506,6 @@ int run_split(const Problem &pr, bool fused, int q_len = 1) {
     return fused ? launch_split<true>(pr.D, p.cols, tk, tv, p, pr.stream)
                  : launch_split<false>(pr.D, p.cols, tk, tv, p, pr.stream);
 }
-
-struct PagedLayout {
-    const int32_t *block_table;
-    int page_size, num_pages, max_pages;
-    bool nhd;
-};
 
 // Paged caches: bf16 (kv_type 0) or 8-bit codes (FD_KV_E4M3 / FD_KV_INT8 with
 // per-kv-head scales), q_len queries per sequence.
@@ -598,33 +544,9 @@ int run_split_paged(const Problem &pr, const PagedLayout &pl, int q_len = 1, int
         }
     }
     const CUtensorMap *rkp = small ? &rk : nullptr, *rvp = small ? &rv : nullptr;
-    fd::SplitParams p;
-    p.q = pr.q;
-    p.seqlens = pr.seqlens;
-    p.out = pr.out;
-    p.lse = pr.lse;
-    seg_pointers(pr, &p.seg_out, &p.seg_lse, &p.row_tickets, q_len);
-    p.chunk_tickets = p.row_tickets ? p.row_tickets + static_cast<size_t>(pr.B) * pr.Hkv : nullptr;
-    p.B = pr.B;
-    p.Hq = pr.Hq;
-    p.Hkv = pr.Hkv;
-    p.g = pr.Hq / pr.Hkv;
-    p.Lmax = pr.max_len;
-    p.P = pr.num_splits;
-    p.q_len = q_len;
-    p.cols = p.g * q_len;
-    p.scale_log2e = pr.scale * kLog2e;
-    p.block_table = pl.block_table;
-    p.max_pages = pl.max_pages;
-    p.page_shift = 0;
-    while ((1 << p.page_shift) < pl.page_size) ++p.page_shift;
-    p.kv_nhd = pl.nhd ? 1 : 0;
-    p.num_pages = pl.num_pages;
+    fd::SplitParams p = split_params(pr, q_len, &pl);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.k_base = p.v_base = nullptr;   // paged pools: no contiguous span to prefetch
-    p.debug_withhold = debug_withhold();
-    p.debug_spoil_guess = debug_spoil_guess();
     if (quant)
         return kv_type == FD_KV_E4M3 ? launch_split_quant<true, true>(pr.D, p.cols, tk, tv, p, pr.stream, rkp, rvp)
                                      : launch_split_quant<false, true>(pr.D, p.cols, tk, tv, p, pr.stream, rkp, rvp);
@@ -651,33 +573,9 @@ int run_split_quant(const Problem &pr, int q_len, int kv_type, const float *k_sc
         if ((rc = encode_cache_map(&tk, pr.k, pr.D, pr.max_len, rows, true)) != FD_OK) return rc;
         if ((rc = encode_cache_map(&tv, pr.v, pr.D, pr.max_len, rows, true)) != FD_OK) return rc;
     }
-    fd::SplitParams p;
-    p.q = pr.q;
-    p.seqlens = pr.seqlens;
-    p.out = pr.out;
-    p.lse = pr.lse;
-    seg_pointers(pr, &p.seg_out, &p.seg_lse, &p.row_tickets, q_len);
-    p.chunk_tickets = p.row_tickets ? p.row_tickets + static_cast<size_t>(pr.B) * pr.Hkv : nullptr;
-    p.B = pr.B;
-    p.Hq = pr.Hq;
-    p.Hkv = pr.Hkv;
-    p.g = pr.Hq / pr.Hkv;
-    p.Lmax = pr.max_len;
-    p.P = pr.num_splits;
-    p.q_len = q_len;
-    p.cols = p.g * q_len;
-    p.scale_log2e = pr.scale * kLog2e;
-    p.block_table = nullptr;
-    p.max_pages = 0;
-    p.page_shift = 0;
-    p.kv_nhd = 0;
-    p.num_pages = 0;
+    fd::SplitParams p = split_params(pr, q_len, nullptr);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.k_base = pr.k;
-    p.v_base = pr.v;
-    p.debug_withhold = debug_withhold();
-    p.debug_spoil_guess = debug_spoil_guess();
     return kv_type == FD_KV_E4M3 ? launch_split_quant<true>(pr.D, p.cols, tk, tv, p, pr.stream)
                                  : launch_split_quant<false>(pr.D, p.cols, tk, tv, p, pr.stream);
 }
@@ -757,7 +655,9 @@ int static_scratch(void **ptr) {
     return FD_OK;
 }
 
-}  // namespace
+}  // namespace fdh
+
+using namespace fdh;
 
 extern "C" {
 
@@ -1065,14 +965,14 @@ int fd_device_status(void *stream) {
         cudaGetLastError();
         return FD_ERR_LAUNCH;
     }
-    int word = 0;
-    const int zero = 0;
-    if (cudaMemcpyFromSymbol(&word, fd::g_fd_error_word, sizeof word) != cudaSuccess ||
-        cudaMemcpyToSymbol(fd::g_fd_error_word, &zero, sizeof zero) != cudaSuccess) {
-        cudaGetLastError();
-        return FD_ERR_LAUNCH;
-    }
-    return word;
+    // each unit that instantiates the split kernel has a word of its own; the first one set is reported
+    int word = 0, other = 0;
+    int rc = take_error_word(fd::g_fd_error_word, &word);
+    if (rc == FD_OK) rc = take_block_error(&other);
+    if (word == FD_OK) word = other;
+    if (rc == FD_OK) rc = take_weights_error(&other);
+    if (word == FD_OK) word = other;
+    return rc != FD_OK ? rc : word;
 }
 
 const char *fd_strerror(int code) {
@@ -1092,6 +992,7 @@ const char *fd_strerror(int code) {
         case FD_ERR_STATIC_LIMIT:
             return "problem needs more scratch than fd_decode_static's fixed 8 MiB buffer; use fd_decode with a workspace";
         case FD_ERR_BOUNDS: return "a debug build's device-side bounds check failed; outputs of that call are invalid";
+        case FD_ERR_OVERLAP: return "an output overlaps an input or another output";
         default: return "unknown error code";
     }
 }

@@ -1,0 +1,365 @@
+// fd_evict.cu -- fd_evict: cut a cache to a budget by accumulated attention
+// weight, in two kernels.
+//
+// Mathematics. For a row (sequence b, kv head h) of L tokens with totals w:
+//   L <= keep: every token stays. Otherwise the last `recent` tokens stay and,
+//   of the M = L - recent others, the k = keep - recent with the largest w
+//   (ties to the lowest index; NaN below everything). Kept tokens stay in
+//   order, so the newest ones are still the last ones.
+// Selection is a radix select on an unsigned key that orders as w does: three
+// passes over 11, 11 and 10 bits from the top, each a histogram of the keys
+// that match the digits found so far, give the k-th largest key; a token is
+// kept if its key is above it, or equal and among the first equal ones. The
+// counts are integers, so nothing depends on the order of the atomics.
+//
+// Select kernel: a cluster of 1 to 8 blocks per row, each with a contiguous
+// slice of its tokens; the histograms are summed over distributed shared
+// memory. Up to 16 keys a thread stay in registers over all passes; longer
+// slices read their totals again from L2.
+// Gather kernel: 16-byte vectors, 64 kept tokens a block, all of a thread's
+// loads in flight before its first store.
+//
+// What bounds it: the kept keys and values, read once and written once
+// (8 D bytes a token); selection reads 4 bytes a cached token and comes
+// before the first copy can start.
+#include <cooperative_groups.h>
+
+#include "fd_host.cuh"
+
+namespace fd {
+
+namespace cg = cooperative_groups;
+
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kKeys = 16;                                   // keys a thread holds
+constexpr int kBatch = kSelectThreads * kKeys;              // tokens of one batch of a slice
+constexpr int kBins = 2048;
+constexpr int kGatherThreads = 256;
+constexpr int kGatherTokens = 64;
+
+struct EvictParams {
+    const uint16_t *k, *v;           // [B, Hkv, Lmax, D]
+    const float *w;                  // [B, Hkv, Lmax]
+    const int32_t *seqlens;          // [B]
+    uint16_t *k_out, *v_out;         // [B, Hkv, out_len, D]
+    float *w_out;                    // [B, Hkv, out_len]
+    int32_t *kept;                   // [B, Hkv, keep]
+    int32_t *seqlens_out;            // [B]
+    int B, Hkv, Lmax, keep, recent, out_len;
+};
+
+// Unsigned order of totals: NaN first, then -inf .. +inf, -0 as +0.
+__device__ __forceinline__ uint32_t order_key(float w) {
+    if (w != w) return 0u;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// Sums of (a, b) over the threads before this one, and the block's totals.
+// Both below 2^16 per block: packed into one word each way.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+        if (lane >= s) incl += y;
+    }
+    __syncthreads();   // the previous use of warp_sums is over
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    uint32_t before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kSelectWarps; ++i) {
+        const uint32_t x = warp_sums[i];
+        before += i < warp ? x : 0u;
+        all += x;
+    }
+    *total = all;
+    return before + incl - v;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictParams p) {
+    __shared__ uint32_t hist[kBins];      // this block's histogram
+    __shared__ uint32_t total[kBins];     // the cluster's
+    __shared__ uint32_t warp_sums[kSelectWarps];
+    __shared__ uint32_t found[3];         // digit, keys above it, keys in it
+    __shared__ uint32_t counts[2];        // kept-above and equal keys of this block's slice
+
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long u = blockIdx.x / C;
+    const int b = static_cast<int>(u / p.Hkv), h = static_cast<int>(u - static_cast<long long>(b) * p.Hkv);
+    const int L = clamp_len(__ldcg(p.seqlens + b), p.Lmax);
+    int32_t *kept = p.kept + static_cast<size_t>(u) * p.keep;
+    const int n = min(L, p.keep);
+    if (h == 0 && rank == 0 && tid == 0) p.seqlens_out[b] = n;
+    const int step = C * kSelectThreads, me = rank * kSelectThreads + tid;
+    if (L <= p.keep) {   // the same in every block of the cluster: nothing to select
+        for (long long i = me; i < p.keep; i += step) kept[i] = i < L ? static_cast<int>(i) : -1;
+        return;
+    }
+    const int M = L - p.recent, k = p.keep - p.recent;
+    for (long long i = me; i < p.recent; i += step) kept[k + i] = static_cast<int>(M + i);
+    if (k == 0) return;
+
+    // this block's slice [lo, hi) of the candidates
+    const long long slice = (static_cast<long long>(M) + C - 1) / C;
+    const int lo = static_cast<int>(min(rank * slice, static_cast<long long>(M)));
+    const int hi = static_cast<int>(min(lo + slice, static_cast<long long>(M)));
+    const float *w = p.w + static_cast<size_t>(u) * p.Lmax;
+    const bool resident = slice <= kBatch;
+    uint32_t key[kKeys];
+    auto load = [&](int base) {   // the batch's keys, thread-striped (token base + i * threads + tid)
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const long long t = static_cast<long long>(base) + i * kSelectThreads + tid;
+            key[i] = t < hi ? order_key(__ldcg(w + t)) : 0u;
+        }
+    };
+    if (resident) load(lo);
+
+    uint32_t prefix = 0, mask = 0, need = static_cast<uint32_t>(k);
+    bool whole_bin = false;   // every key that matches the prefix is kept
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && !whole_bin; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t dmask = pass == 2 ? 1023u : 2047u;
+        for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+        __syncthreads();
+        for (long long base = lo; base < hi; base += kBatch) {
+            if (!resident) load(static_cast<int>(base));
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) {
+                const long long t = base + i * kSelectThreads + tid;
+                if (t < hi && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & dmask], 1u);
+            }
+        }
+        // the cluster's histogram, in every block: block r sums its share of
+        // the bins over all blocks and hands it to all of them
+        if (C > 1) {
+            cluster.sync();
+            const int share = kBins / C;
+            for (int i = tid; i < share; i += kSelectThreads) {
+                const int bin = rank * share + i;
+                uint32_t s = 0;
+                for (int r = 0; r < C; ++r) s += cluster.map_shared_rank(hist, r)[bin];
+                for (int r = 0; r < C; ++r) cluster.map_shared_rank(total, r)[bin] = s;
+            }
+            cluster.sync();
+        } else {
+            __syncthreads();
+        }
+        const uint32_t *bins = C > 1 ? total : hist;
+        // the digit whose bin holds the need-th key from the top: each thread
+        // takes 4 bins, the highest first
+        constexpr int kPer = kBins / kSelectThreads;
+        uint32_t c[kPer], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            c[i] = bins[kBins - 1 - (tid * kPer + i)];
+            mine += c[i];
+        }
+        // counts can pass 2^16 here: one word holds one count
+        uint32_t all, before = block_exclusive(mine, warp_sums, &all);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (before < need && before + c[i] >= need) {
+                found[0] = static_cast<uint32_t>(kBins - 1 - (tid * kPer + i));
+                found[1] = before;
+                found[2] = c[i];
+            }
+            before += c[i];
+        }
+        __syncthreads();
+        prefix |= found[0] << shift;
+        mask |= dmask << shift;
+        need -= found[1];
+        whole_bin = found[2] == need;
+        __syncthreads();   // found and hist are written again by the next pass
+    }
+    // kept: (key & mask) > prefix, and the first `need` with (key & mask) == prefix
+
+    // this slice's counts, then those of the slices before it
+    uint32_t gt = 0, eq = 0;
+    for (long long base = lo; base < hi; base += kBatch) {
+        if (!resident) load(static_cast<int>(base));
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const long long t = base + i * kSelectThreads + tid;
+            if (t < hi) {
+                gt += (key[i] & mask) > prefix;
+                eq += (key[i] & mask) == prefix;
+            }
+        }
+    }
+    uint32_t gt_all, eq_all;
+    block_exclusive(gt, warp_sums, &gt_all);
+    block_exclusive(eq, warp_sums, &eq_all);
+    uint32_t gt_before = 0, eq_before = 0;
+    if (C > 1) {
+        if (tid == 0) {
+            counts[0] = gt_all;
+            counts[1] = eq_all;
+        }
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            gt_before += cluster.map_shared_rank(counts, r)[0];
+            eq_before += cluster.map_shared_rank(counts, r)[1];
+        }
+    }
+
+    // ranks in token order: a warp's ballot, the warps' counts, the steps
+    for (long long base = lo; base < hi; base += kBatch) {
+        if (!resident) load(static_cast<int>(base));
+#pragma unroll 1
+        for (int i = 0; i < kKeys; ++i) {
+            const long long t = base + i * kSelectThreads + tid;
+            if (base + i * kSelectThreads >= hi) break;
+            uint32_t kk = 0;   // key[i] without indexing registers at run time
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) kk = j == i ? key[j] : kk;
+            const bool g = t < hi && (kk & mask) > prefix, e = t < hi && (kk & mask) == prefix;
+            const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+            __syncthreads();
+            if (lane == 0) warp_sums[warp] = static_cast<uint32_t>(__popc(bg)) | (static_cast<uint32_t>(__popc(be)) << 16);
+            __syncthreads();
+            uint32_t before = 0, all = 0;   // at most 512 of each kind: 16 bits hold them
+#pragma unroll
+            for (int j = 0; j < kSelectWarps; ++j) {
+                const uint32_t x = warp_sums[j];
+                before += j < warp ? x : 0u;
+                all += x;
+            }
+            const unsigned lower = (1u << lane) - 1u;
+            const uint32_t gb = gt_before + (before & 0xffffu) + __popc(bg & lower);
+            const uint32_t eb = eq_before + (before >> 16) + __popc(be & lower);
+            if (g || (e && eb < need)) kept[gb + min(eb, need)] = static_cast<int>(t);
+            gt_before += all & 0xffffu;
+            eq_before += all >> 16;
+        }
+    }
+    if (C > 1) cluster.sync();   // no block leaves while another reads its shared memory
+}
+
+template <int D>
+__global__ void __launch_bounds__(kGatherThreads) fd_gather_kernel(const EvictParams p, long long chunks, long long total) {
+    constexpr int kVec = D / 8;                                     // 16-byte vectors of a token
+    constexpr int NI = kGatherTokens * kVec / kGatherThreads;       // vectors per thread, of K and of V
+    constexpr int kRows = kGatherThreads / kVec;
+    __shared__ int idx[kGatherTokens];
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int tid = threadIdx.x, row0 = tid / kVec, col = (tid % kVec) * 8;
+    for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+        const long long u = item / chunks;
+        const int s0 = static_cast<int>((item - u * chunks) * kGatherTokens);
+        const int b = static_cast<int>(u / p.Hkv);
+        const int n = min(clamp_len(__ldcg(p.seqlens + b), p.Lmax), p.keep);
+        __syncthreads();
+        if (tid < kGatherTokens && s0 + tid < p.out_len) {
+            const int s = s0 + tid;
+            const int t = s < n ? __ldcg(p.kept + static_cast<size_t>(u) * p.keep + s) : 0;
+            idx[tid] = t;
+            p.w_out[static_cast<size_t>(u) * p.out_len + s] = s < n ? __ldcg(p.w + static_cast<size_t>(u) * p.Lmax + t) : 0.f;
+        }
+        __syncthreads();
+        if (s0 >= n) continue;
+        const uint16_t *k = p.k + static_cast<size_t>(u) * p.Lmax * D + col;
+        const uint16_t *v = p.v + static_cast<size_t>(u) * p.Lmax * D + col;
+        uint4 x[NI], y[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = row0 + i * kRows;
+            if (s0 + r < n) {
+                const size_t at = static_cast<size_t>(idx[r]) * D;
+                x[i] = __ldcs(reinterpret_cast<const uint4 *>(k + at));
+                y[i] = __ldcs(reinterpret_cast<const uint4 *>(v + at));
+            }
+        }
+        const size_t out = (static_cast<size_t>(u) * p.out_len + s0) * D + col;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = row0 + i * kRows;
+            if (s0 + r < n) {
+                *reinterpret_cast<uint4 *>(p.k_out + out + static_cast<size_t>(r) * D) = x[i];
+                *reinterpret_cast<uint4 *>(p.v_out + out + static_cast<size_t>(r) * D) = y[i];
+            }
+        }
+    }
+}
+
+}  // namespace fd
+
+
+extern "C" {
+
+int fd_evict(int B, int Hkv, int D, int max_len, int keep, int recent, int out_len, const uint16_t *k_cache,
+             const uint16_t *v_cache, const float *weights, const int32_t *seqlens, uint16_t *k_out, uint16_t *v_out,
+             float *weights_out, int32_t *kept, int32_t *seqlens_out, void *stream) {
+    using namespace fdh;
+    int rc = check_shape(B, Hkv, Hkv, D, max_len);
+    if (rc != FD_OK) return rc;
+    if (keep < 1 || recent < 0 || recent > keep || out_len < keep) return FD_ERR_SHAPE;
+    if (!seqlens || !k_out || !v_out || !weights_out || !kept || !seqlens_out) return FD_ERR_NULL_POINTER;
+    if (max_len > 0 && (!k_cache || !v_cache || !weights)) return FD_ERR_NULL_POINTER;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return FD_ERR_ALIGNMENT;
+    if (!aligned(weights, 4) || !aligned(weights_out, 4) || !aligned(kept, 4) || !aligned(seqlens, 4) ||
+        !aligned(seqlens_out, 4))
+        return FD_ERR_ALIGNMENT;
+    // the blocks copy in no order: what is written may not be what another still reads
+    const size_t rows = static_cast<size_t>(B) * Hkv;
+    const size_t in_b = rows * max_len * D * 2, out_b = rows * out_len * D * 2;
+    const size_t win_b = rows * max_len * 4, wout_b = rows * out_len * 4, kept_b = rows * keep * 4;
+    const size_t len_b = static_cast<size_t>(B) * 4;
+    const void *ins[4] = {k_cache, v_cache, weights, seqlens};
+    const size_t in_n[4] = {in_b, in_b, win_b, len_b};
+    const void *outs[5] = {k_out, v_out, weights_out, kept, seqlens_out};
+    const size_t out_n[5] = {out_b, out_b, wout_b, kept_b, len_b};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap(outs[i], out_n[i], ins[j], in_n[j])) return FD_ERR_OVERLAP;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FD_ERR_OVERLAP;
+    }
+    if (rows * 8 > 0x7fffffffULL) return FD_ERR_SHAPE;   // grid x of the select kernel
+    int sms;
+    if ((rc = device_sms(&sms)) != FD_OK) return rc;
+
+    fd::EvictParams p;
+    p.k = k_cache;
+    p.v = v_cache;
+    p.w = weights;
+    p.seqlens = seqlens;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.w_out = weights_out;
+    p.kept = kept;
+    p.seqlens_out = seqlens_out;
+    p.B = B;
+    p.Hkv = Hkv;
+    p.Lmax = max_len;
+    p.keep = keep;
+    p.recent = recent;
+    p.out_len = out_len;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // blocks per row: more while a slice is longer than 2048 tokens and the
+    // rows leave SMs idle
+    int C = 1;
+    while (C < 8 && max_len / C > 2048 && static_cast<long long>(rows) * C * 2 <= 2LL * sms) C *= 2;
+    if ((rc = launch_dependent(fd::fd_select_kernel, dim3(static_cast<unsigned>(rows * C)), fd::kSelectThreads, 0, st, C,
+                               p)) != FD_OK)
+        return rc;
+    const long long chunks = (static_cast<long long>(out_len) + fd::kGatherTokens - 1) / fd::kGatherTokens;
+    const long long total = static_cast<long long>(rows) * chunks;
+    const dim3 grid(static_cast<unsigned>(total < 0x7fffffffLL ? total : 0x7fffffffLL));
+    return D == 128 ? launch_dependent(fd::fd_gather_kernel<128>, grid, fd::kGatherThreads, 0, st, 1, p, chunks, total)
+                    : launch_dependent(fd::fd_gather_kernel<64>, grid, fd::kGatherThreads, 0, st, 1, p, chunks, total);
+}
+
+}  // extern "C"

@@ -23,8 +23,9 @@
 namespace fd {
 
 // Sticky per-device error word (FD_ERR_TIMEOUT when a wait gave up,
-// FD_ERR_BOUNDS when a debug build's bounds check failed).
-__device__ int g_fd_error_word;
+// FD_ERR_BOUNDS when a debug build's bounds check failed); one per
+// translation unit, all read by fd_device_status.
+static __device__ int g_fd_error_word;
 
 // Debug builds (-DFD_DEBUG) check the global accesses whose indices come
 // from the partition arithmetic; a failed check records FD_ERR_BOUNDS and

@@ -45,13 +45,29 @@
 //     small probabilities stay normal f16 numbers; the running sum carries
 //     the same factor, so the normalised output is unchanged and only the
 //     log-sum-exp is corrected (m - kPScale).
+//
+// One scale per block of T tokens and kv head (kBlock; T a power of two from
+// 16 up, so a scale covers whole 16-token blocks of a warp's slice):
+//     x_t = scale log2(e) k_scale[t / T] (q . decode(k_t)),
+//     out = sum_t 2^(x_t - m) v_scale[t / T] decode(v_t) / sum_t 2^(x_t - m).
+//   * The key scale multiplies the block's logits. The value scale joins the
+//     weight's exponent: with y_t = x_t + log2 v_scale[t / T], P V takes
+//     2^(y_t - mo) and the sum 2^(x_t - m), each with a lazy reference maximum
+//     of its own, both moved by the same rare branch. So whatever the scales'
+//     spread, P keeps its f16 range relative to the row's largest
+//     contribution; a zero scale gives y = -inf, weight 0. This costs a second
+//     2^x per (token, column), 4 of about 200 issue slots a thread spends on
+//     a tile at up to 8 columns.
+//   * A warp reads its 16-token blocks' scales (through the block table for
+//     paged caches) one tile of its group ahead, with loads from L2, so their
+//     latency lies behind a tile's arithmetic.
 #pragma once
 
 #include "fd_split.cuh"
 
 namespace fd {
 
-template <int D, int NT, bool kE4M3, int kTok = 16>
+template <int D, int NT, bool kE4M3, int kTok = 16, bool kBlock = false, bool kPagedScales = false>
 struct QuantConsumer {
     static constexpr int G = 8 * NT;        // columns held (padded)
     static constexpr int kElemBytes = 1;
@@ -59,6 +75,7 @@ struct QuantConsumer {
     static constexpr int MB = kTok / 16;              // 16-token blocks per warp
     static constexpr int KACC = MB == 1 ? 2 : 1;      // logit accumulators per block
     static constexpr bool kInterleaved = false;
+    static constexpr bool kTileHook = kBlock;
     static constexpr int KC = D / 16;       // 16-byte chunks of a token = k-steps of S = m-tiles of O^T
     static constexpr int kRowBytes = D;
     // The reference max lags the running max by at most kLazy (base 2), so
@@ -73,6 +90,11 @@ struct QuantConsumer {
     int shift[NT][2];                       // causal offset of columns 2c, 2c+1
     float colmul[NT][2];                    // logit multiplier (base 2) of columns 2c, 2c+1
     float kmul, vmul;                       // scale * log2(e) * k_scale[h], and v_scale[h]
+    // kBlock only
+    float mo[NT][2];                        // reference max of y = x + log2 v_scale, columns 2c, 2c+1
+    float ks[MB], lv[MB];                   // this tile's key scales and log2 of its value scales
+    float ks_next[MB], vs_next[MB];         // the group's next tile's scales, on their way
+    int page_next[MB];                      // paged: the pages of the tile after that
 
     __device__ __forceinline__ void init(const SplitParams &p) {
         const int cc = (threadIdx.x & 31) & 3;
@@ -86,8 +108,74 @@ struct QuantConsumer {
     }
 
     __device__ __forceinline__ void set_row(const SplitParams &p, int h) {
-        kmul = p.scale_log2e * __ldg(p.k_scale + h);
-        vmul = __ldg(p.v_scale + h);
+        if constexpr (kBlock) {
+            kmul = p.scale_log2e;
+            vmul = 1.f;
+        } else {
+            kmul = p.scale_log2e * __ldg(p.k_scale + h);
+            vmul = __ldg(p.v_scale + h);
+        }
+    }
+
+    // Pages of the slice's 16-token blocks from token t0 on; -1 past the row
+    // (t0 < 0: no such tile) and for entries outside the pool.
+    __device__ __forceinline__ void fetch_pages(const SplitParams &p, int b, int t0, int L) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            const int t = t0 + 16 * mb;
+            page_next[mb] = -1;
+            if (t0 >= 0 && t < L && FD_DCHECK(b < p.B && (t >> p.page_shift) < p.max_pages))
+                page_next[mb] = __ldcg(p.block_table + static_cast<size_t>(b) * p.max_pages + (t >> p.page_shift));
+        }
+    }
+
+    // Start the loads of the scales of the slice's 16-token blocks from token
+    // t0 on; 0 for blocks past the row. L2 loads: the kernel before this one
+    // on the stream may have written them after this grid began.
+    __device__ __forceinline__ void fetch_scales(const SplitParams &p, const Cursor &c, int t0, int L) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            const int t = t0 + 16 * mb;
+            ks_next[mb] = vs_next[mb] = 0.f;
+            if (t0 < 0 || t >= L) continue;
+            size_t at;
+            if constexpr (kPagedScales) {
+                const int page = page_next[mb];
+                if (page < 0 || page >= p.num_pages) continue;   // reads as a page of zeros
+                at = (static_cast<size_t>(page) * p.Hkv + c.h) * p.blocks +
+                     ((t & ((1 << p.page_shift) - 1)) >> p.blk_shift);
+            } else {
+                at = (static_cast<size_t>(c.b) * p.Hkv + c.h) * p.blocks + (t >> p.blk_shift);
+                if (!FD_DCHECK((t >> p.blk_shift) < p.blocks)) continue;
+            }
+            ks_next[mb] = __ldcg(p.k_scale + at);
+            vs_next[mb] = __ldcg(p.v_scale + at);
+        }
+    }
+
+    // Segment start: the scales of the group's first tile (t0: first token of
+    // this warp's slice in it).
+    __device__ __forceinline__ void start_segment(const SplitParams &p, const Cursor &c, int t0, int, int L) {
+        if constexpr (kPagedScales) {
+            fetch_pages(p, c.b, t0, L);
+            fetch_scales(p, c, t0, L);
+            fetch_pages(p, c.b, t0 + kTileTokens * (kConsumerWarps * kTok / kTileTokens), L);
+        } else {
+            fetch_scales(p, c, t0, L);
+        }
+    }
+
+    // Before a tile: its scales have been asked for a tile ago; ask for those
+    // of the group's next one (first token t_next, -1 if the segment ends).
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int, int t_next, int L) {
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+            ks[mb] = ks_next[mb];
+            lv[mb] = lg2(vs_next[mb]);
+        }
+        fetch_scales(p, c, t_next, L);
+        if constexpr (kPagedScales)
+            fetch_pages(p, c.b, t_next < 0 ? -1 : t_next + kTileTokens * (kConsumerWarps * kTok / kTileTokens), L);
     }
 
     __device__ __forceinline__ void reset() {
@@ -95,6 +183,7 @@ struct QuantConsumer {
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
+            if constexpr (kBlock) mo[nt][0] = mo[nt][1] = -INFINITY;
 #pragma unroll
             for (int c = 0; c < KC; ++c) o[nt][c][0] = o[nt][c][1] = o[nt][c][2] = o[nt][c][3] = 0.f;
         }
@@ -223,7 +312,7 @@ struct QuantConsumer {
                 for (int e = 0; e < 4; ++e) {
                     float acc = s[mb][0][nt][e];
                     if (KACC == 2) acc += s[mb][KACC - 1][nt][e];
-                    x[mb][nt][e] = acc * colmul[nt][e & 1];
+                    x[mb][nt][e] = acc * (kBlock ? colmul[nt][e & 1] * ks[mb] : colmul[nt][e & 1]);
                 }
                 // token r of this block is inside column e's causal range when r < valid - 16 mb - shift
                 const int va = valid - 16 * mb - shift[nt][0], vb = valid - 16 * mb - shift[nt][1];
@@ -231,30 +320,51 @@ struct QuantConsumer {
                 if (r0 >= vb) x[mb][nt][1] = -INFINITY;
                 if (r0 + 8 >= va) x[mb][nt][2] = -INFINITY;
                 if (r0 + 8 >= vb) x[mb][nt][3] = -INFINITY;
-                const float ta = m[nt][0] + kLazy, tb = m[nt][1] + kLazy;
+                float ta = m[nt][0] + kLazy, tb = m[nt][1] + kLazy;
+                if constexpr (kBlock) {   // y = x + lv against its own reference (a zero scale never moves it)
+                    ta = fminf(ta, mo[nt][0] + kLazy - lv[mb]);
+                    tb = fminf(tb, mo[nt][1] + kLazy - lv[mb]);
+                }
                 grow |= x[mb][nt][0] > ta || x[mb][nt][2] > ta || x[mb][nt][1] > tb || x[mb][nt][3] > tb;
             }
         if (__any_sync(0xffffffffu, grow)) {   // the fallback: a synchronised rescale
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float ma = -INFINITY, mbx = -INFINITY;
+                float ya = -INFINITY, yb = -INFINITY;   // kBlock: the same of y
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
-                    ma = fmaxf(ma, fmaxf(x[mb][nt][0], x[mb][nt][2]));
-                    mbx = fmaxf(mbx, fmaxf(x[mb][nt][1], x[mb][nt][3]));
+                    const float xa = fmaxf(x[mb][nt][0], x[mb][nt][2]), xb = fmaxf(x[mb][nt][1], x[mb][nt][3]);
+                    ma = fmaxf(ma, xa);
+                    mbx = fmaxf(mbx, xb);
+                    if constexpr (kBlock) {
+                        ya = fmaxf(ya, xa + lv[mb]);
+                        yb = fmaxf(yb, xb + lv[mb]);
+                    }
                 }
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) {
                     ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
                     mbx = fmaxf(mbx, __shfl_xor_sync(0xffffffffu, mbx, sh));
+                    if constexpr (kBlock) {
+                        ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, sh));
+                        yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, sh));
+                    }
                 }
                 const float na = fmaxf(m[nt][0], ma), nb = fmaxf(m[nt][1], mbx);
                 const float ua = na == -INFINITY ? 0.f : na, ub = nb == -INFINITY ? 0.f : nb;
-                const float alpha_a = ex2(m[nt][0] - ua), alpha_b = ex2(m[nt][1] - ub);
+                float alpha_a = ex2(m[nt][0] - ua), alpha_b = ex2(m[nt][1] - ub);
                 l[nt][0] *= alpha_a;
                 l[nt][1] *= alpha_b;
                 m[nt][0] = na;
                 m[nt][1] = nb;
+                if constexpr (kBlock) {   // the accumulators go by y's reference
+                    const float oa = fmaxf(mo[nt][0], ya), ob = fmaxf(mo[nt][1], yb);
+                    alpha_a = ex2(mo[nt][0] - (oa == -INFINITY ? 0.f : oa));
+                    alpha_b = ex2(mo[nt][1] - (ob == -INFINITY ? 0.f : ob));
+                    mo[nt][0] = oa;
+                    mo[nt][1] = ob;
+                }
 #pragma unroll
                 for (int c = 0; c < KC; ++c) {
                     o[nt][c][0] *= alpha_a;
@@ -269,14 +379,22 @@ struct QuantConsumer {
         uint32_t bh[MB][NT][2], bl[MB][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float ta = kPScale - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
-            const float tb = kPScale - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+            float ta = kPScale - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
+            float tb = kPScale - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                const float p0 = ex2(x[mb][nt][0] + ta), p2 = ex2(x[mb][nt][2] + ta);
-                const float p1 = ex2(x[mb][nt][1] + tb), p3 = ex2(x[mb][nt][3] + tb);
+                float p0 = ex2(x[mb][nt][0] + ta), p2 = ex2(x[mb][nt][2] + ta);
+                float p1 = ex2(x[mb][nt][1] + tb), p3 = ex2(x[mb][nt][3] + tb);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
+                if constexpr (kBlock) {   // P V's weights: 2^(y - mo), with the same 2^kPScale
+                    const float ya = kPScale + lv[mb] - (mo[nt][0] == -INFINITY ? 0.f : mo[nt][0]);
+                    const float yb = kPScale + lv[mb] - (mo[nt][1] == -INFINITY ? 0.f : mo[nt][1]);
+                    p0 = ex2(x[mb][nt][0] + ya);
+                    p2 = ex2(x[mb][nt][2] + ya);
+                    p1 = ex2(x[mb][nt][1] + yb);
+                    p3 = ex2(x[mb][nt][3] + yb);
+                }
                 const uint32_t h01 = pack_f16x2(p0, p1), h23 = pack_f16x2(p2, p3);
                 const uint32_t l01 = pack_f16x2(p0 - f16lo_to_f32(h01), p1 - f16hi_to_f32(h01));
                 const uint32_t l23 = pack_f16x2(p2 - f16lo_to_f32(h23), p3 - f16hi_to_f32(h23));
@@ -338,13 +456,18 @@ struct QuantConsumer {
 #pragma unroll
                 for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
             const int ha = nt * 8 + 2 * cc, hb = ha + 1;
+            float va = vmul, vb = vmul;
+            if constexpr (kBlock) {   // from y's reference back to x's; no contribution at all: 0
+                va = mo[nt][0] == -INFINITY ? 0.f : ex2(mo[nt][0] - m[nt][0]);
+                vb = mo[nt][1] == -INFINITY ? 0.f : ex2(mo[nt][1] - m[nt][1]);
+            }
             // dims d0 and d0 + 1 of one head as one 8-byte store; with the padded
             // head stride the 16 lanes of each half warp fill all 32 banks
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const int d0 = 16 * c + dlo;
-                *reinterpret_cast<float2 *>(wb + ha * S + d0) = make_float2(o[nt][c][0] * vmul, o[nt][c][2] * vmul);
-                *reinterpret_cast<float2 *>(wb + hb * S + d0) = make_float2(o[nt][c][1] * vmul, o[nt][c][3] * vmul);
+                *reinterpret_cast<float2 *>(wb + ha * S + d0) = make_float2(o[nt][c][0] * va, o[nt][c][2] * va);
+                *reinterpret_cast<float2 *>(wb + hb * S + d0) = make_float2(o[nt][c][1] * vb, o[nt][c][3] * vb);
             }
             if (r0 == 0) {
                 wb[G * S + ha] = m[nt][0] == -INFINITY ? -INFINITY : m[nt][0] - kPScale;

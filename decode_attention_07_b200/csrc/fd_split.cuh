@@ -109,6 +109,12 @@ struct SplitParams {
     // contiguous caches only: the K and V arrays, for the bulk L2 prefetch before the dependency wait
     const void *k_base;
     const void *v_base;
+    // 8-bit caches with one scale per block of tokens: k_scale / v_scale are [B, Hkv, blocks]
+    // or, for paged caches, [num_pages, Hkv, blocks], blocks = scale blocks of a row or of a page
+    int blk_shift;            // log2(tokens per scale block)
+    int blocks;
+    // attention-weight accumulation only
+    float *logits;            // [B, Hkv, Lmax, logit_cols<cols>]: base-2 logits of every column, for the pass after
     int debug_withhold;       // debug builds: block 0 issues no copy for this tile (a wait then runs out); -1: off
     int debug_spoil_guess;    // debug builds: make every block's pre-wait guess of its start wrong
 };
@@ -120,6 +126,10 @@ __device__ __forceinline__ size_t out_rows(const SplitParams &p) {
 __device__ __forceinline__ size_t seg_rows(const SplitParams &p) {
     return (static_cast<size_t>(p.P) + static_cast<size_t>(p.B) * p.Hkv - 1) * p.cols;
 }
+
+// Columns a token's logits take in SplitParams::logits: even above one, so
+// that the grouped consumer stores column pairs as 8 bytes.
+__host__ __device__ __forceinline__ int logit_cols(int cols) { return cols == 1 ? 1 : (cols + 1) & ~1; }
 
 constexpr int kPageWindow = 1024;                 // block-table entries staged in shared memory
 
@@ -500,7 +510,8 @@ __device__ __forceinline__ void merge_warps_and_store(const float *merge, float 
 }
 
 // ------------------------------------------------- grouped-head consumer --
-template <int D, int NT, bool kInter = false>
+// kLogits: also write the (masked, base-2) logits of every column to memory.
+template <int D, int NT, bool kInter = false, bool kLogits = false>
 struct GroupConsumer {
     static constexpr int KS = D / 16;   // k-steps of the logit contraction
     static constexpr int MT = D / 16;   // m-tiles of the P V contraction
@@ -508,7 +519,10 @@ struct GroupConsumer {
     static constexpr int kElemBytes = 2;
     static constexpr int kWarpTokens = 16;
     static constexpr bool kInterleaved = kInter;
+    static constexpr bool kTileHook = kLogits;
 
+    float *lg;                          // kLogits: logits of this warp's slice of the tile, [token][lcols]
+    int lcols;
     uint32_t qf[NT][KS][2];             // Q^T as the B operand, per n-tile
     float m[NT][2], l[NT][2];           // running max (base 2) / partial sum for heads 2c, 2c+1
     float o[NT][MT][4];                 // O^T accumulators
@@ -526,6 +540,13 @@ struct GroupConsumer {
     }
 
     __device__ __forceinline__ void set_row(const SplitParams &, int) {}   // bf16 cache: no per-head scales
+
+    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int, int) {}
+    // Before the tile of row tokens [t0, t0 + 16) of this warp: where its logits go.
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0, int, int) {
+        lcols = logit_cols(p.cols);
+        lg = p.logits + ((static_cast<size_t>(c.b) * p.Hkv + c.h) * p.Lmax + t0) * lcols;
+    }
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -601,6 +622,13 @@ struct GroupConsumer {
             if (r0 >= vb) x1 = -INFINITY;
             if (r0 + 8 >= va) x2 = -INFINITY;
             if (r0 + 8 >= vb) x3 = -INFINITY;
+            if constexpr (kLogits) {   // column pairs, tokens inside the row only
+                const int col = nt * 8 + 2 * cc;
+                if (col < lcols) {
+                    if (r0 < valid) *reinterpret_cast<float2 *>(lg + r0 * lcols + col) = make_float2(x0, x1);
+                    if (r0 + 8 < valid) *reinterpret_cast<float2 *>(lg + (r0 + 8) * lcols + col) = make_float2(x2, x3);
+                }
+            }
             float ma = fmaxf(x0, x2), mb = fmaxf(x1, x3);
 #pragma unroll
             for (int sh = 4; sh < 32; sh <<= 1) {
@@ -686,7 +714,8 @@ struct GroupConsumer {
 // kTok tokens of each tile per warp: 16 (four warps per group, two groups) or
 // 32 (two warps per group, four groups), the 32 as two 16-token halves whose
 // dependency chains interleave and which share one rescale of the state.
-template <int D, bool kInter = false, int kTok = 16>
+// kLogits: also write the (masked, base-2) logits to memory.
+template <int D, bool kInter = false, int kTok = 16, bool kLogits = false>
 struct HeadConsumer {
     static constexpr int G = 1;
     static constexpr int kElemBytes = 2;
@@ -697,13 +726,19 @@ struct HeadConsumer {
     static constexpr int ITER = 16 / TPI;      // warp-wide loads per 16-token half
     static constexpr int NSUB = kTok / 16;     // 16-token halves
     static_assert(kTok == 16 || kTok == 32, "16 or 32 tokens per warp");
+    static constexpr bool kTileHook = kLogits;
 
+    float *lg;                                 // kLogits: logits of this warp's slice of the tile
     uint4 qw;                                  // q[d0 .. d0+7] of this lane's 16-byte chunk (bf16 pairs)
     float m, l;                                // running max (base 2, warp-uniform) / lane partial sum
     float acc[8];                              // sum of p * v over this lane's tokens, chunk d0..d0+7
 
     __device__ __forceinline__ void init(const SplitParams &) {}   // one query, one head: no offsets
     __device__ __forceinline__ void set_row(const SplitParams &, int) {}
+    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int, int) {}
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0, int, int) {
+        lg = p.logits + (static_cast<size_t>(c.b) * p.Hkv + c.h) * p.Lmax + t0;
+    }
 
     __device__ __forceinline__ void reset() {
         m = -INFINITY;
@@ -774,6 +809,7 @@ struct HeadConsumer {
         for (int s = 0; s < NSUB; ++s) {
             x[s] = (pd[s][0] + __shfl_xor_sync(0xffffffffu, pd[s][0], 1)) * scale_log2e;
             if (16 * s + TPI * my_it + half >= valid) x[s] = -INFINITY;
+            else if (kLogits && (lane & 1) == 0) lg[16 * s + TPI * my_it + half] = x[s];   // one lane of the pair
             mx = fmaxf(mx, x[s]);
         }
 #pragma unroll
@@ -1237,10 +1273,18 @@ __global__ void __launch_bounds__(split_threads<kPaged>(), 1)
             const int L = clamp_len(__ldg(p.seqlens + c.b), p.Lmax);
             cons.reset();
             cons.set_row(p, c.h);
+            if constexpr (Consumer::kTileHook) {   // first tile of this group in the segment
+                const int k0 = (group - static_cast<int>(seq % kGroupsC) + kGroupsC) % kGroupsC;
+                if (k0 < seg) cons.start_segment(p, c, (c.tile + k0) * kTileTokens + kTok * slice, slice, L);
+            }
             for (int k = 0; k < seg; ++k, ++seq) {
                 if (static_cast<int>(seq % kGroupsC) != group) continue;
                 const int stage = static_cast<int>(seq % kStages);
                 const uint32_t phase = (seq / kStages) & 1u;
+                if constexpr (Consumer::kTileHook) {   // first token of this warp's slice; the same in the group's next tile
+                    const int t0 = (c.tile + k) * kTileTokens + kTok * slice;
+                    cons.before_tile(p, c, t0, k + kGroupsC < seg ? t0 + kGroupsC * kTileTokens : -1, L);
+                }
                 wait_bounded(&full[stage], phase, abort);   // on abort: keep going, outputs are flagged invalid
                 const uint8_t *st = ring + stage * Cfg::kStageBytes;
                 if (k < kGroupsC) cons.load_q(st + 2 * Cfg::kTileBytes, p.cols);

@@ -92,6 +92,8 @@ extern "C" {
 #define FD_ERR_BOUNDS       -13   /* debug builds only (-DFD_DEBUG): a device-side bounds check failed; the
                                      access was skipped and the call's outputs are invalid */
 
+#define FD_ERR_OVERLAP      -14   /* an output overlaps an input or another output (fd_decode_weights, fd_evict) */
+
 #define FD_TILE_TOKENS     64     /* tokens per tile; split boundaries are multiples of this */
 #define FD_MAX_SPLITS      65535
 #define FD_MAX_GROUP       16
@@ -259,6 +261,119 @@ FD_API int fd_decode_quant_paged(int B, int q_len, int Hq, int Hkv, int D, int p
                                  const float *v_scale, const int32_t *block_table, const int32_t *seqlens,
                                  float scale, float *out, float *lse, void *workspace, size_t workspace_bytes,
                                  int num_splits, void *stream);
+
+/* ---- cache compression: hold a cache in 8 bits, score its tokens, evict ---- */
+
+/* fd_decode_quant over a cache with one scale per BLOCK of block_tokens
+ * tokens and kv head, so that a block's codes span its own range: the cached
+ * key of token t of sequence b, kv head h is
+ *     k_scale[b][h][t / block_tokens] * decode(k_codes[b][h][t][:]),
+ * the value likewise. k_scale / v_scale: [B][Hkv][ceil(max_len /
+ * block_tokens)] float32, device, 4-byte aligned, finite and >= 0 for every
+ * block that holds a cached token (0 stands for a block of zeros); those of
+ * other blocks are never used, whatever they hold. block_tokens: 16, 32, 64
+ * or 128. The key scale enters the block's logits and the value scale the
+ * exponent of the block's weights, so scales of any spread keep their
+ * precision relative to the row's largest contribution (a scale below the
+ * smallest normal float counts as 0). Everything else, codes, queries,
+ * workspace, errors, as in fd_decode_quant; FD_ERR_SHAPE also for
+ * block_tokens. */
+FD_API int fd_decode_quant_block(int B, int q_len, int Hq, int Hkv, int D, int max_len, int block_tokens, int kv_type,
+                                 const uint16_t *q, const uint8_t *k_codes, const uint8_t *v_codes,
+                                 const float *k_scale, const float *v_scale, const int32_t *seqlens, float scale,
+                                 float *out, float *lse, void *workspace, size_t workspace_bytes, int num_splits,
+                                 void *stream);
+
+/* fd_decode_quant_block over PAGED pools: codes as in fd_decode_quant_paged
+ * (either kv_layout), scales [num_pages][Hkv][page_size / block_tokens] for
+ * both layouts, found through the same block table. block_tokens <=
+ * page_size (so page_size >= 16). An entry outside the pool reads as a page
+ * of zeros and its scales are not read. */
+FD_API int fd_decode_quant_block_paged(int B, int q_len, int Hq, int Hkv, int D, int page_size, int num_pages,
+                                       int max_pages_per_seq, int kv_layout, int block_tokens, int kv_type,
+                                       const uint16_t *q, const uint8_t *k_pages, const uint8_t *v_pages,
+                                       const float *k_scale, const float *v_scale, const int32_t *block_table,
+                                       const int32_t *seqlens, float scale, float *out, float *lse, void *workspace,
+                                       size_t workspace_bytes, int num_splits, void *stream);
+
+/* Append bf16 tokens to such a cache: a whole prompt, a chunk or one token
+ * per sequence. Token j of sequence b, kv head h is the D contiguous elements
+ * at k_new + b*stride_b + j*stride_t + h*stride_h (strides in elements,
+ * multiples of 8; pointers 16-byte aligned; v_new likewise, same strides).
+ * seqlens[b] counts the cached tokens INCLUDING the new ones, as for
+ * fd_decode_multi, so one tensor serves the append and the decode after it:
+ * sequence b has n = n_new new tokens, or new_lens[b] clamped to [0, n_new]
+ * where new_lens is not NULL, and token j goes to position seqlens[b] - n + j.
+ * Positions outside [0, max_len) are dropped. For each block of block_tokens
+ * positions that gets new tokens, with a = the largest magnitude among them
+ * and R = 448 (FD_KV_E4M3) or 127 (FD_KV_INT8):
+ *     s    = a / R rounded up to 8 significant bits;
+ *     a block that also holds older tokens keeps max(its scale, s), and if
+ *     that grew, its older codes become round(decode(code) * old / new);
+ *     new codes = round(x / scale), half to even (codes 0 where a = 0).
+ * So each growth of a block's scale re-rounds its older tokens, by at most
+ * half a step of the new scale. Every quotient rounds as the real number
+ * does, ties included. New tokens must be finite, and the scale of a block
+ * that holds older tokens finite and >= 0. Codes and scales of all other
+ * positions and blocks are left as they were. One kernel on `stream`; no
+ * workspace.
+ * n_new = 0 or max_len = 0: nothing to do, no CUDA call. */
+FD_API int fd_quant_append(int B, int n_new, int Hkv, int D, int max_len, int block_tokens, int kv_type,
+                           const uint16_t *k_new, const uint16_t *v_new, long long stride_b, long long stride_t,
+                           long long stride_h, const int32_t *new_lens, const int32_t *seqlens, uint8_t *k_codes,
+                           uint8_t *v_codes, float *k_scale, float *v_scale, void *stream);
+
+/* fd_quant_append into PAGED pools (fd_decode_quant_block_paged's layouts).
+ * Blocks whose block-table entry is outside the pool are dropped. A page that
+ * gets new tokens must belong to one sequence of the call. */
+FD_API int fd_quant_append_paged(int B, int n_new, int Hkv, int D, int page_size, int num_pages,
+                                 int max_pages_per_seq, int kv_layout, int block_tokens, int kv_type,
+                                 const uint16_t *k_new, const uint16_t *v_new, long long stride_b,
+                                 long long stride_t, long long stride_h, const int32_t *new_lens,
+                                 const int32_t *block_table, const int32_t *seqlens, uint8_t *k_pages,
+                                 uint8_t *v_pages, float *k_scale, float *v_scale, void *stream);
+
+/* fd_decode_multi that also returns each cached token's attention weight,
+ * summed over the query heads of its kv head and over the q_len queries, added
+ * to a running total:
+ *     weights_out[b][h][t] = weights_in[b][h][t] + sum_{j, i} exp(z - lse)
+ * over queries j that see token t and query heads i of kv head h, for t <
+ * seqlens[b]; later positions of weights_out are left as they were.
+ * weights_in / weights_out: [B][Hkv][max_len] fp32, device, 4-byte aligned;
+ * weights_in NULL counts as zeros, and may be weights_out itself (a total
+ * kept in place) but not overlap it otherwise. out, lse: those of
+ * fd_decode_multi. Two kernels on `stream`. Workspace:
+ * fd_weights_workspace_bytes(), of which 4 bytes per (cached position, column
+ * of its kv head) hold logits; zero before its first use, as for fd_decode,
+ * and again before it serves another shape. */
+FD_API size_t fd_weights_workspace_bytes(int B, int q_len, int Hq, int Hkv, int D, int max_len, int num_splits);
+FD_API int fd_decode_weights(int B, int q_len, int Hq, int Hkv, int D, int max_len,
+                             const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                             const int32_t *seqlens, float scale, float *out, float *lse, const float *weights_in,
+                             float *weights_out, void *workspace, size_t workspace_bytes, int num_splits,
+                             void *stream);
+
+/* Cut a bf16 cache to a budget of `keep` tokens per (sequence, kv head) by
+ * such totals. A row of L = seqlens[b] (clamped to [0, max_len]) tokens with
+ * L <= keep stays whole; otherwise its last `recent` tokens stay and, of the
+ * others, the keep - recent with the largest `weights` (ties to the lowest
+ * position; NaN counts as the smallest). With n = min(L, keep), kept tokens
+ * in their order:
+ *     kept[b][h][0..n)        their positions, the rest of [0, keep) -1
+ *     k_out, v_out[b][h][0..n) their keys and values; later rows left as they were
+ *     weights_out[b][h][0..n)  their totals, the rest of [0, out_len) 0 (what
+ *                              tokens appended there later start from)
+ *     seqlens_out[b]           n
+ * k_cache, v_cache [B][Hkv][max_len][D], k_out, v_out [B][Hkv][out_len][D]
+ * bf16, 16-byte aligned; weights [B][Hkv][max_len], weights_out
+ * [B][Hkv][out_len] fp32; kept [B][Hkv][keep], seqlens, seqlens_out [B] int32.
+ * D 64 or 128, 1 <= keep <= out_len, 0 <= recent <= keep. Outputs may not
+ * overlap the inputs or one another (FD_ERR_OVERLAP). Two kernels on
+ * `stream`; no workspace. */
+FD_API int fd_evict(int B, int Hkv, int D, int max_len, int keep, int recent, int out_len,
+                    const uint16_t *k_cache, const uint16_t *v_cache, const float *weights, const int32_t *seqlens,
+                    uint16_t *k_out, uint16_t *v_out, float *weights_out, int32_t *kept, int32_t *seqlens_out,
+                    void *stream);
 
 /* Split stage alone (one kernel): for each run of tiles, writes out/lse of
  * the rows it holds whole and the segments of the rows it holds in part.
