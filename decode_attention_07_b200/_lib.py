@@ -584,9 +584,11 @@ def _one_device(*tensors):
     return devices.pop()
 
 
-def _prepared(what, device, args):
+def _prepared(what, tensors, args):
     """A no-argument callable that runs entry point `what` with `args`, with
-    `device` (where the tensors are) as the current device."""
+    the device of `tensors` as the current one. It holds the tensors (None
+    entries aside): their memory stays theirs as long as it lives."""
+    device = _one_device(*tensors)
     fn = getattr(lib(), what)
     # converted once here, not on every call
     args = tuple(t(a) if a is not None else a for t, a in zip(fn.argtypes, args))
@@ -600,6 +602,7 @@ def _prepared(what, device, args):
         if rc != 0:
             raise FdError(rc, what)
 
+    call.tensors = tensors
     return call
 
 
@@ -672,9 +675,9 @@ def prepare_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, b
     _block_outputs(q, out, lse)
     _seqlens(seqlens, B)
     wp, wb = _ws(workspace)
-    dev = _one_device(q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, workspace)
-    S = _planned(dev, B, Hq, Hkv, D, Lmax, num_splits)
-    call = _prepared("fd_decode_quant_block", dev, (
+    tensors = (q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, workspace)
+    S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
+    call = _prepared("fd_decode_quant_block", tensors, (
         B, q_len, Hq, Hkv, D, Lmax, block_tokens, KV_CODES[kv_type], q.data_ptr(), k_codes.data_ptr(),
         v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(),
         lse.data_ptr(), wp, wb, S, _stream(stream, q.device)))
@@ -717,9 +720,9 @@ def prepare_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_t
     _block_outputs(q, out, lse)
     _seqlens(seqlens, B)
     wp, wb = _ws(workspace)
-    dev = _one_device(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
-    S = _planned(dev, B, Hq, Hkv, D, max_pages * page_size, num_splits)
-    call = _prepared("fd_decode_quant_block_paged", dev, (
+    tensors = (q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
+    S = _planned(q.device.index, B, Hq, Hkv, D, max_pages * page_size, num_splits)
+    call = _prepared("fd_decode_quant_block_paged", tensors, (
         B, q_len, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], block_tokens, KV_CODES[kv_type],
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         block_table.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, S,
@@ -789,8 +792,8 @@ def prepare_quant_append(k_new, v_new, k_codes, v_codes, k_scale, v_scale, kv_ty
     B, Hkv, Lmax, D = _block_codes(k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens)
     n_new, (sb, st, sh) = _new_tokens(k_new, v_new, B, Hkv, D)
     lens = _append_lens(new_lens, seqlens, B)
-    dev = _one_device(k_new, v_new, k_codes, v_codes, k_scale, v_scale, seqlens, new_lens)
-    return _prepared("fd_quant_append", dev, (
+    tensors = (k_new, v_new, k_codes, v_codes, k_scale, v_scale, seqlens, new_lens)
+    return _prepared("fd_quant_append", tensors, (
         B, n_new, Hkv, D, Lmax, block_tokens, KV_CODES[kv_type], k_new.data_ptr(), v_new.data_ptr(), sb, st, sh, lens,
         seqlens.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         _stream(stream, k_new.device)))
@@ -812,8 +815,8 @@ def prepare_quant_append_paged(k_new, v_new, k_pages, v_pages, k_scale, v_scale,
     B = block_table.shape[0]
     n_new, (sb, st, sh) = _new_tokens(k_new, v_new, B, Hkv, D)
     lens = _append_lens(new_lens, seqlens, B)
-    dev = _one_device(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, new_lens)
-    return _prepared("fd_quant_append_paged", dev, (
+    tensors = (k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, new_lens)
+    return _prepared("fd_quant_append_paged", tensors, (
         B, n_new, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], block_tokens, KV_CODES[kv_type],
         k_new.data_ptr(), v_new.data_ptr(), sb, st, sh, lens, block_table.data_ptr(), seqlens.data_ptr(),
         k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), _stream(stream, k_new.device)))
@@ -856,9 +859,9 @@ def prepare_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weight
         if t is not None or name == "weights_out":
             _tensor(t, name, (B, Hkv, Lmax), torch.float32)
     wp, wb = _ws(workspace)
-    dev = _one_device(q, k_cache, v_cache, seqlens, out, lse, weights_in, weights_out, workspace)
-    S = _planned(dev, B, Hq, Hkv, D, Lmax, num_splits)
-    call = _prepared("fd_decode_weights", dev, (
+    tensors = (q, k_cache, v_cache, seqlens, out, lse, weights_in, weights_out, workspace)
+    S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
+    call = _prepared("fd_decode_weights", tensors, (
         B, q_len, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
         float(scale), out.data_ptr(), lse.data_ptr(), None if weights_in is None else weights_in.data_ptr(),
         weights_out.data_ptr(), wp, wb, S, _stream(stream, q.device)))
@@ -912,8 +915,8 @@ def prepare_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out
     _tensor(kept, "kept", (B, Hkv, keep), torch.int32)
     for t, name in ((seqlens, "seqlens"), (seqlens_out, "seqlens_out")):
         _tensor(t, name, (B,), torch.int32)
-    dev = _one_device(k_cache, v_cache, weights, seqlens, k_out, v_out, weights_out, kept, seqlens_out)
-    return _prepared("fd_evict", dev, (
+    tensors = (k_cache, v_cache, weights, seqlens, k_out, v_out, weights_out, kept, seqlens_out)
+    return _prepared("fd_evict", tensors, (
         B, Hkv, D, Lmax, keep, recent, out_len, k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(),
         seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), weights_out.data_ptr(), kept.data_ptr(),
         seqlens_out.data_ptr(), _stream(stream, k_cache.device)))

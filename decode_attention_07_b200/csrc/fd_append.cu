@@ -23,14 +23,16 @@
 //
 // What bounds it: 4 D bytes read and 2 D written per (token, kv head); for a
 // token or two, the launch and two dependent loads (length, then data).
-// One 128-thread block per (block of tokens, kv head, K or V): the block's
-// new tokens stay in registers (16 bytes a load, up to 16 loads in flight a
-// thread) between the maximum and the rounding, so they are read once.
+// A group of 1 to 8 warps per (block of tokens, kv head, K or V), 8 loads of
+// 16 bytes in flight a thread: the new tokens stay in registers between the
+// maximum and the rounding, so they are read once. 256 threads a block: the
+// groups of neighbouring heads, whose tokens lie side by side in a
+// token-major source.
 #include "fd_host.cuh"
 
 namespace fd {
 
-constexpr int kAppendThreads = 128;
+constexpr int kAppendThreads = 256;
 
 struct AppendParams {
     const uint16_t *src[2];          // k_new, v_new
@@ -108,17 +110,25 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
     v[3] = f16hi_to_f32(hi);
 }
 
+// Threads per (block of tokens, head): 8 chunks of 16 bytes each.
+template <int D, int T>
+__host__ __device__ constexpr int append_group() {
+    return T * D / 64 < 32 ? 32 : T * D / 64;
+}
+
 template <int D, int T, bool kE4M3, bool kPaged>
 __global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const AppendParams p) {
     constexpr int kVec = D / 8;                       // 16-byte chunks of a token
-    constexpr int NI = T * kVec / kAppendThreads;     // chunks per thread
-    constexpr int kRows = kAppendThreads / kVec;      // tokens per step
-    static_assert(NI >= 1, "a block of tokens fills the threads");
+    constexpr int kGroup = append_group<D, T>();      // threads of a group
+    constexpr int kGroups = kAppendThreads / kGroup;  // heads of a block
+    constexpr int NI = T * kVec / kGroup;             // chunks per thread
+    constexpr int kRows = kGroup / kVec;              // tokens per step
     __shared__ float warp_max[kAppendThreads / 32];
     grid_dependents_launch();
     grid_dependency_wait();
-    const int tid = threadIdx.x;
-    const int h = blockIdx.x >> 1, kv = blockIdx.x & 1;
+    const int tid = threadIdx.x % kGroup, group = threadIdx.x / kGroup;
+    const int h = (blockIdx.x >> 1) * kGroups + group, kv = blockIdx.x & 1;
+    if (h >= p.Hkv) return;
     const int row0 = tid / kVec, col = (tid % kVec) * 8;
     for (long long b = blockIdx.z; b < p.B; b += gridDim.z) {
         const long long end = __ldcg(p.seqlens + b);
@@ -173,11 +183,14 @@ __global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const AppendP
             float a = fmaxf(__low2float(m2), __high2float(m2));
 #pragma unroll
             for (int sh = 16; sh > 0; sh >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, sh));
-            __syncthreads();   // the last block's maxima have been read
-            if ((tid & 31) == 0) warp_max[tid >> 5] = a;
-            __syncthreads();
+            if constexpr (kGroup > 32) {   // over the group's warps
+                float *wm = warp_max + group * (kGroup / 32);
+                named_barrier_sync(1 + group, kGroup);   // the last maxima have been read
+                if ((tid & 31) == 0) wm[tid >> 5] = a;
+                named_barrier_sync(1 + group, kGroup);
 #pragma unroll
-            for (int w = 0; w < kAppendThreads / 32; ++w) a = fmaxf(a, warp_max[w]);
+                for (int w = 0; w < kGroup / 32; ++w) a = fmaxf(a, wm[w]);
+            }
 
             const float s = fmaxf(block_scale<kE4M3>(a), s_old);
             if (tid == 0 && !(has_old && s == s_old)) p.scale[kv][scale_at] = s;
@@ -242,7 +255,8 @@ namespace {
 
 template <int D, int T, bool kE4M3>
 int launch_append(const fd::AppendParams &p, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>(p.Hkv) * 2u, static_cast<unsigned>(p.touched < 65535 ? p.touched : 65535),
+    constexpr int heads = fd::kAppendThreads / fd::append_group<D, T>();
+    const dim3 grid(static_cast<unsigned>((p.Hkv + heads - 1) / heads) * 2u, static_cast<unsigned>(p.touched < 65535 ? p.touched : 65535),
                     static_cast<unsigned>(p.B < 65535 ? p.B : 65535));
     return p.block_table ? launch_dependent(fd::fd_append_kernel<D, T, kE4M3, true>, grid, fd::kAppendThreads, 0, st, 1, p)
                          : launch_dependent(fd::fd_append_kernel<D, T, kE4M3, false>, grid, fd::kAppendThreads, 0, st, 1,

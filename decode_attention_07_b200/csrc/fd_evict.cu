@@ -6,16 +6,19 @@
 //   of the M = L - recent others, the k = keep - recent with the largest w
 //   (ties to the lowest index; NaN below everything). Kept tokens stay in
 //   order, so the newest ones are still the last ones.
-// Selection is a radix select on an unsigned key that orders as w does: three
-// passes over 11, 11 and 10 bits from the top, each a histogram of the keys
-// that match the digits found so far, give the k-th largest key; a token is
-// kept if its key is above it, or equal and among the first equal ones. The
-// counts are integers, so nothing depends on the order of the atomics.
+// Selection is a radix select on an unsigned key that orders as w does: four
+// passes over 8 bits from the top, each a histogram of the keys that match the
+// digits found so far, give the k-th largest key; a token is kept if its key
+// is above it, or equal and among the first equal ones. The counts are
+// integers, so nothing depends on the order of the atomics.
 //
 // Select kernel: a cluster of 1 to 8 blocks per row, each with a contiguous
-// slice of its tokens; the histograms are summed over distributed shared
-// memory. Up to 16 keys a thread stay in registers over all passes; longer
-// slices read their totals again from L2.
+// slice of its tokens; a pass exchanges 256 bins over distributed shared
+// memory. Totals crowd into few digits (a few binades, many zeros), so each
+// lane has its own column of bins: a warp's 32 additions never meet (one
+// shared column per block measured 75 us on a 131072-token row, all of it
+// additions to the same few words). Up to 16 keys a thread stay in registers
+// over all passes; longer slices read their totals again from L2.
 // Gather kernel: 16-byte vectors, 64 kept tokens a block, all of a thread's
 // loads in flight before its first store.
 //
@@ -34,7 +37,7 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kKeys = 16;                                   // keys a thread holds
 constexpr int kBatch = kSelectThreads * kKeys;              // tokens of one batch of a slice
-constexpr int kBins = 2048;
+constexpr int kBins = 256;
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 64;
 
@@ -56,36 +59,13 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// Sums of (a, b) over the threads before this one, and the block's totals.
-// Both below 2^16 per block: packed into one word each way.
-__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t *warp_sums, uint32_t *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t incl = v;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += y;
-    }
-    __syncthreads();   // the previous use of warp_sums is over
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kSelectWarps; ++i) {
-        const uint32_t x = warp_sums[i];
-        before += i < warp ? x : 0u;
-        all += x;
-    }
-    *total = all;
-    return before + incl - v;
-}
-
 __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[kBins];      // this block's histogram
-    __shared__ uint32_t total[kBins];     // the cluster's
+    __shared__ uint32_t hist[kBins * 32];        // this block's histogram, one column of bins per lane
+    __shared__ uint32_t bins[2][kBins];          // its sums, by turns: the cluster reads one while the next is made
+    __shared__ uint32_t counts[kKeys * kSelectWarps];   // a batch's (above | equal << 16) by step and warp
     __shared__ uint32_t warp_sums[kSelectWarps];
-    __shared__ uint32_t found[3];         // digit, keys above it, keys in it
-    __shared__ uint32_t counts[2];        // kept-above and equal keys of this block's slice
+    __shared__ uint32_t found[3];                // digit, keys above it, keys in it
+    __shared__ uint32_t slice_sums[2];           // kept-above and equal keys of this block's slice
 
     cg::cluster_group cluster = cg::this_cluster();
     const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -126,122 +106,144 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
     uint32_t prefix = 0, mask = 0, need = static_cast<uint32_t>(k);
     bool whole_bin = false;   // every key that matches the prefix is kept
 #pragma unroll 1
-    for (int pass = 0; pass < 3 && !whole_bin; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-        const uint32_t dmask = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+    for (int pass = 0; pass < 4 && !whole_bin; ++pass) {
+        const int shift = 24 - 8 * pass;
+        for (int i = tid; i < kBins * 32 / 4; i += kSelectThreads) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         for (long long base = lo; base < hi; base += kBatch) {
             if (!resident) load(static_cast<int>(base));
 #pragma unroll
             for (int i = 0; i < kKeys; ++i) {
                 const long long t = base + i * kSelectThreads + tid;
-                if (t < hi && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & dmask], 1u);
+                if (t < hi && (key[i] & mask) == prefix) atomicAdd(&hist[((key[i] >> shift) & 255u) * 32 + lane], 1u);
             }
         }
-        // the cluster's histogram, in every block: block r sums its share of
-        // the bins over all blocks and hands it to all of them
-        if (C > 1) {
+        __syncthreads();
+        uint32_t *mine = bins[pass & 1];
+#pragma unroll
+        for (int i = 0; i < kBins / kSelectWarps; ++i) {
+            const int bin = warp * (kBins / kSelectWarps) + i;
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, hist[bin * 32 + lane]);
+            if (lane == 0) mine[bin] = sum;
+        }
+        // the digit whose bin holds the need-th key of the cluster from the
+        // top: thread i looks at bin 255 - i. The other block's bins of this
+        // pass are whole after the cluster barrier, and written again two
+        // passes on, after the next one.
+        if (C > 1)
             cluster.sync();
-            const int share = kBins / C;
-            for (int i = tid; i < share; i += kSelectThreads) {
-                const int bin = rank * share + i;
-                uint32_t s = 0;
-                for (int r = 0; r < C; ++r) s += cluster.map_shared_rank(hist, r)[bin];
-                for (int r = 0; r < C; ++r) cluster.map_shared_rank(total, r)[bin] = s;
-            }
-            cluster.sync();
-        } else {
+        else
             __syncthreads();
-        }
-        const uint32_t *bins = C > 1 ? total : hist;
-        // the digit whose bin holds the need-th key from the top: each thread
-        // takes 4 bins, the highest first
-        constexpr int kPer = kBins / kSelectThreads;
-        uint32_t c[kPer], mine = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            c[i] = bins[kBins - 1 - (tid * kPer + i)];
-            mine += c[i];
-        }
-        // counts can pass 2^16 here: one word holds one count
-        uint32_t all, before = block_exclusive(mine, warp_sums, &all);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (before < need && before + c[i] >= need) {
-                found[0] = static_cast<uint32_t>(kBins - 1 - (tid * kPer + i));
-                found[1] = before;
-                found[2] = c[i];
+        uint32_t c = 0, incl = 0;
+        if (tid < kBins) {
+            const int bin = kBins - 1 - tid;
+            if (C > 1) {
+#pragma unroll 8
+                for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(mine, r)[bin];
+            } else {
+                c = mine[bin];
             }
-            before += c[i];
+            incl = c;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s) incl += y;
+            }
+            if (lane == 31) warp_sums[warp] = incl;
+        }
+        __syncthreads();
+        if (tid < kBins) {
+            uint32_t before = incl - c;
+            for (int i = 0; i < warp; ++i) before += warp_sums[i];
+            if (before < need && before + c >= need) {
+                found[0] = static_cast<uint32_t>(kBins - 1 - tid);
+                found[1] = before;
+                found[2] = c;
+            }
         }
         __syncthreads();
         prefix |= found[0] << shift;
-        mask |= dmask << shift;
+        mask |= 255u << shift;
         need -= found[1];
         whole_bin = found[2] == need;
-        __syncthreads();   // found and hist are written again by the next pass
+        // (found is written again only after the next pass's barriers)
     }
     // kept: (key & mask) > prefix, and the first `need` with (key & mask) == prefix
 
-    // this slice's counts, then those of the slices before it
-    uint32_t gt = 0, eq = 0;
-    for (long long base = lo; base < hi; base += kBatch) {
-        if (!resident) load(static_cast<int>(base));
+    // a batch's counts by step and warp -> exclusive sums in token order;
+    // returns the batch's total (all packed: at most 8192 of each kind)
+    auto rank_batch = [&](long long base) -> uint32_t {
+        __syncthreads();   // the last batch's sums have been read
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const long long t = base + i * kSelectThreads + tid;
-            if (t < hi) {
-                gt += (key[i] & mask) > prefix;
-                eq += (key[i] & mask) == prefix;
-            }
+            const bool in = base + i * kSelectThreads + tid < hi;
+            const unsigned bg = __ballot_sync(0xffffffffu, in && (key[i] & mask) > prefix);
+            const unsigned be = __ballot_sync(0xffffffffu, in && (key[i] & mask) == prefix);
+            if (lane == 0) counts[i * kSelectWarps + warp] = static_cast<uint32_t>(__popc(bg)) | (static_cast<uint32_t>(__popc(be)) << 16);
         }
-    }
-    uint32_t gt_all, eq_all;
-    block_exclusive(gt, warp_sums, &gt_all);
-    block_exclusive(eq, warp_sums, &eq_all);
+        __syncthreads();
+        uint32_t c = 0, incl = 0;
+        if (tid < kKeys * kSelectWarps) {
+            c = counts[tid];
+            incl = c;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, s);
+                if (lane >= s) incl += y;
+            }
+            if (lane == 31) warp_sums[warp] = incl;
+        }
+        __syncthreads();
+        uint32_t total = 0;
+        uint32_t before = incl - c;
+#pragma unroll
+        for (int i = 0; i < kKeys * kSelectWarps / 32; ++i) {
+            const uint32_t x = warp_sums[i];
+            before += i < warp ? x : 0u;
+            total += x;
+        }
+        if (tid < kKeys * kSelectWarps) counts[tid] = before;
+        __syncthreads();
+        return total;
+    };
+    static_assert(kKeys * kSelectWarps <= kSelectThreads && kKeys * kSelectWarps % 32 == 0, "one scan of the counts");
+    static_assert(kBatch < 65536, "packed counts");
+
     uint32_t gt_before = 0, eq_before = 0;
-    if (C > 1) {
+    if (C > 1) {   // this slice's counts, then those of the slices before it
+        uint32_t gt = 0, eq = 0;
+        for (long long base = lo; base < hi; base += kBatch) {
+            if (!resident) load(static_cast<int>(base));
+            const uint32_t t = rank_batch(base);
+            gt += t & 0xffffu;
+            eq += t >> 16;
+        }
         if (tid == 0) {
-            counts[0] = gt_all;
-            counts[1] = eq_all;
+            slice_sums[0] = gt;
+            slice_sums[1] = eq;
         }
         cluster.sync();
         for (int r = 0; r < rank; ++r) {
-            gt_before += cluster.map_shared_rank(counts, r)[0];
-            eq_before += cluster.map_shared_rank(counts, r)[1];
+            gt_before += cluster.map_shared_rank(slice_sums, r)[0];
+            eq_before += cluster.map_shared_rank(slice_sums, r)[1];
         }
     }
-
-    // ranks in token order: a warp's ballot, the warps' counts, the steps
     for (long long base = lo; base < hi; base += kBatch) {
         if (!resident) load(static_cast<int>(base));
-#pragma unroll 1
+        const uint32_t total = rank_batch(base);
+        const unsigned lower = (1u << lane) - 1u;
+#pragma unroll
         for (int i = 0; i < kKeys; ++i) {
             const long long t = base + i * kSelectThreads + tid;
-            if (base + i * kSelectThreads >= hi) break;
-            uint32_t kk = 0;   // key[i] without indexing registers at run time
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j) kk = j == i ? key[j] : kk;
-            const bool g = t < hi && (kk & mask) > prefix, e = t < hi && (kk & mask) == prefix;
+            const bool g = t < hi && (key[i] & mask) > prefix, e = t < hi && (key[i] & mask) == prefix;
             const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-            __syncthreads();
-            if (lane == 0) warp_sums[warp] = static_cast<uint32_t>(__popc(bg)) | (static_cast<uint32_t>(__popc(be)) << 16);
-            __syncthreads();
-            uint32_t before = 0, all = 0;   // at most 512 of each kind: 16 bits hold them
-#pragma unroll
-            for (int j = 0; j < kSelectWarps; ++j) {
-                const uint32_t x = warp_sums[j];
-                before += j < warp ? x : 0u;
-                all += x;
-            }
-            const unsigned lower = (1u << lane) - 1u;
+            const uint32_t before = counts[i * kSelectWarps + warp];
             const uint32_t gb = gt_before + (before & 0xffffu) + __popc(bg & lower);
             const uint32_t eb = eq_before + (before >> 16) + __popc(be & lower);
             if (g || (e && eb < need)) kept[gb + min(eb, need)] = static_cast<int>(t);
-            gt_before += all & 0xffffu;
-            eq_before += all >> 16;
         }
+        gt_before += total & 0xffffu;
+        eq_before += total >> 16;
     }
     if (C > 1) cluster.sync();   // no block leaves while another reads its shared memory
 }

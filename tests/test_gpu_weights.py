@@ -146,6 +146,21 @@ def test_two_graphs_with_their_own_workspaces():
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(acc, want[2])
 
 
+def test_a_prepared_call_keeps_its_tensors():
+    q, k, v, w, lens = make(1, 1, 4, 2, 500, 64, [500], 7)
+    ws = torch.zeros(fd.fd_weights_workspace_bytes(1, 1, 4, 2, 64, 500, 5), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:-1], device="cuda")
+    call = fd.prepare_decode_weights(q, k, v, lens, 0.1, out, lse, None, w, ws, 5)
+    assert any(t is ws for t in call.tensors) and any(t is k for t in call.tensors)
+    want = fd.decode_weights(q, k, v, lens, 0.1, num_splits=5)
+    del ws, k, v
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    call()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
 def test_binding_refusals():
     q, k, v, w, lens = make(1, 1, 4, 2, 100, 64, [100], 6)
     with pytest.raises(ValueError):
