@@ -33,10 +33,8 @@ namespace fd {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kKeys = 16;                                   // keys a thread holds
-constexpr int kBatch = kSelectThreads * kKeys;              // tokens of one batch of a slice
+constexpr int kKeys = 16;                                   // keys a thread of the select kernel holds
+constexpr int kShortSlice = 256 * kKeys;                    // slices that 256 threads hold
 constexpr int kBins = 256;
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 64;
@@ -59,11 +57,17 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictParams p) {
+// kT threads: 256 for slices of up to 4096 tokens (more rows at once on an
+// SM), 1024 for longer ones.
+template <int kT>
+__global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
+    constexpr int kWarps = kT / 32;
+    constexpr int kBatch = kT * kKeys;           // tokens of one batch of a slice
+    constexpr int kCounts = kKeys * kWarps;
     __shared__ uint32_t hist[kBins * 32];        // this block's histogram, one column of bins per lane
     __shared__ uint32_t bins[2][kBins];          // its sums, by turns: the cluster reads one while the next is made
-    __shared__ uint32_t counts[kKeys * kSelectWarps];   // a batch's (above | equal << 16) by step and warp
-    __shared__ uint32_t warp_sums[kSelectWarps];
+    __shared__ uint32_t counts[kCounts];        // a batch's (above | equal << 16) by step and warp
+    __shared__ uint32_t warp_sums[kWarps];
     __shared__ uint32_t found[3];                // digit, keys above it, keys in it
     __shared__ uint32_t slice_sums[2];           // kept-above and equal keys of this block's slice
 
@@ -78,7 +82,7 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
     int32_t *kept = p.kept + static_cast<size_t>(u) * p.keep;
     const int n = min(L, p.keep);
     if (h == 0 && rank == 0 && tid == 0) p.seqlens_out[b] = n;
-    const int step = C * kSelectThreads, me = rank * kSelectThreads + tid;
+    const int step = C * kT, me = rank * kT + tid;
     if (L <= p.keep) {   // the same in every block of the cluster: nothing to select
         for (long long i = me; i < p.keep; i += step) kept[i] = i < L ? static_cast<int>(i) : -1;
         return;
@@ -94,12 +98,16 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
     const float *w = p.w + static_cast<size_t>(u) * p.Lmax;
     const bool resident = slice <= kBatch;
     uint32_t key[kKeys];
-    auto load = [&](int base) {   // the batch's keys, thread-striped (token base + i * threads + tid)
+    // the batch's keys, thread-striped: token base + i * kT + tid, inside the
+    // slice while i * kT < left(base)
+    auto left = [&](long long base) { return static_cast<int>(min(hi - base, static_cast<long long>(kBatch))) - tid; };
+    auto load = [&](long long base) {
+        const int n_left = left(base);
+        const float *at = w + base + tid;
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-            const long long t = static_cast<long long>(base) + i * kSelectThreads + tid;
-            key[i] = t < hi ? order_key(__ldcg(w + t)) : 0u;
-        }
+        for (int i = 0; i < kKeys; ++i) key[i] = i * kT < n_left ? __float_as_uint(__ldcg(at + i * kT)) : 0u;
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) key[i] = order_key(__uint_as_float(key[i]));
     };
     if (resident) load(lo);
 
@@ -108,21 +116,21 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
 #pragma unroll 1
     for (int pass = 0; pass < 4 && !whole_bin; ++pass) {
         const int shift = 24 - 8 * pass;
-        for (int i = tid; i < kBins * 32 / 4; i += kSelectThreads) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < kBins * 32 / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         for (long long base = lo; base < hi; base += kBatch) {
-            if (!resident) load(static_cast<int>(base));
+            if (!resident) load(base);
+            const int n_left = left(base);
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) {
-                const long long t = base + i * kSelectThreads + tid;
-                if (t < hi && (key[i] & mask) == prefix) atomicAdd(&hist[((key[i] >> shift) & 255u) * 32 + lane], 1u);
-            }
+            for (int i = 0; i < kKeys; ++i)
+                if (i * kT < n_left && (key[i] & mask) == prefix)
+                    atomicAdd(&hist[((key[i] >> shift) & 255u) * 32 + lane], 1u);
         }
         __syncthreads();
         uint32_t *mine = bins[pass & 1];
 #pragma unroll
-        for (int i = 0; i < kBins / kSelectWarps; ++i) {
-            const int bin = warp * (kBins / kSelectWarps) + i;
+        for (int i = 0; i < kBins / kWarps; ++i) {
+            const int bin = warp * (kBins / kWarps) + i;
             const uint32_t sum = __reduce_add_sync(0xffffffffu, hist[bin * 32 + lane]);
             if (lane == 0) mine[bin] = sum;
         }
@@ -170,20 +178,28 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
     }
     // kept: (key & mask) > prefix, and the first `need` with (key & mask) == prefix
 
-    // a batch's counts by step and warp -> exclusive sums in token order;
-    // returns the batch's total (all packed: at most 8192 of each kind)
+    // The batch's tokens above the threshold and equal to it, as bits of two
+    // masks a thread; their counts by step and warp become exclusive sums in
+    // token order (packed above | equal << 16: at most 16384 of each kind).
+    // Returns the batch's total.
+    uint32_t gt_bits = 0, eq_bits = 0;
     auto rank_batch = [&](long long base) -> uint32_t {
+        const int n_left = left(base);
+        gt_bits = eq_bits = 0;
         __syncthreads();   // the last batch's sums have been read
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const bool in = base + i * kSelectThreads + tid < hi;
-            const unsigned bg = __ballot_sync(0xffffffffu, in && (key[i] & mask) > prefix);
-            const unsigned be = __ballot_sync(0xffffffffu, in && (key[i] & mask) == prefix);
-            if (lane == 0) counts[i * kSelectWarps + warp] = static_cast<uint32_t>(__popc(bg)) | (static_cast<uint32_t>(__popc(be)) << 16);
+            const uint32_t kk = key[i] & mask;
+            const bool in = i * kT < n_left, g = in && kk > prefix, e = in && kk == prefix;
+            gt_bits |= g ? 1u << i : 0u;
+            eq_bits |= e ? 1u << i : 0u;
+            const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, g))) |
+                               (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, e))) << 16);
+            if (lane == 0) counts[i * kWarps + warp] = n;
         }
         __syncthreads();
         uint32_t c = 0, incl = 0;
-        if (tid < kKeys * kSelectWarps) {
+        if (tid < kCounts) {
             c = counts[tid];
             incl = c;
 #pragma unroll
@@ -194,29 +210,28 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
             if (lane == 31) warp_sums[warp] = incl;
         }
         __syncthreads();
-        uint32_t total = 0;
-        uint32_t before = incl - c;
+        uint32_t total = 0, before = incl - c;
 #pragma unroll
-        for (int i = 0; i < kKeys * kSelectWarps / 32; ++i) {
+        for (int i = 0; i < kCounts / 32; ++i) {
             const uint32_t x = warp_sums[i];
             before += i < warp ? x : 0u;
             total += x;
         }
-        if (tid < kKeys * kSelectWarps) counts[tid] = before;
+        if (tid < kCounts) counts[tid] = before;
         __syncthreads();
         return total;
     };
-    static_assert(kKeys * kSelectWarps <= kSelectThreads && kKeys * kSelectWarps % 32 == 0, "one scan of the counts");
+    static_assert(kCounts <= kT && kCounts % 32 == 0, "one scan of the counts");
     static_assert(kBatch < 65536, "packed counts");
 
-    uint32_t gt_before = 0, eq_before = 0;
+    uint32_t gt_before = 0, eq_before = 0, total = 0;
     if (C > 1) {   // this slice's counts, then those of the slices before it
         uint32_t gt = 0, eq = 0;
         for (long long base = lo; base < hi; base += kBatch) {
-            if (!resident) load(static_cast<int>(base));
-            const uint32_t t = rank_batch(base);
-            gt += t & 0xffffu;
-            eq += t >> 16;
+            if (!resident) load(base);
+            total = rank_batch(base);
+            gt += total & 0xffffu;
+            eq += total >> 16;
         }
         if (tid == 0) {
             slice_sums[0] = gt;
@@ -228,19 +243,19 @@ __global__ void __launch_bounds__(kSelectThreads) fd_select_kernel(const EvictPa
             eq_before += cluster.map_shared_rank(slice_sums, r)[1];
         }
     }
+    const unsigned lower = (1u << lane) - 1u;
     for (long long base = lo; base < hi; base += kBatch) {
-        if (!resident) load(static_cast<int>(base));
-        const uint32_t total = rank_batch(base);
-        const unsigned lower = (1u << lane) - 1u;
+        if (!resident) load(base);
+        if (C == 1 || !resident) total = rank_batch(base);   // (one batch: still there)
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const long long t = base + i * kSelectThreads + tid;
-            const bool g = t < hi && (key[i] & mask) > prefix, e = t < hi && (key[i] & mask) == prefix;
+            const bool g = (gt_bits >> i) & 1u, e = (eq_bits >> i) & 1u;
             const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
-            const uint32_t before = counts[i * kSelectWarps + warp];
+            if ((bg | be) == 0) continue;
+            const uint32_t before = counts[i * kWarps + warp];
             const uint32_t gb = gt_before + (before & 0xffffu) + __popc(bg & lower);
             const uint32_t eb = eq_before + (before >> 16) + __popc(be & lower);
-            if (g || (e && eb < need)) kept[gb + min(eb, need)] = static_cast<int>(t);
+            if (g || (e && eb < need)) kept[gb + min(eb, need)] = static_cast<int>(base) + i * kT + tid;
         }
         gt_before += total & 0xffffu;
         eq_before += total >> 16;
@@ -350,13 +365,15 @@ int fd_evict(int B, int Hkv, int D, int max_len, int keep, int recent, int out_l
     p.recent = recent;
     p.out_len = out_len;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // blocks per row: more while a slice is longer than 2048 tokens and the
+    // blocks per row: more while a slice is longer than 4096 tokens and the
     // rows leave SMs idle
     int C = 1;
-    while (C < 8 && max_len / C > 2048 && static_cast<long long>(rows) * C * 2 <= 2LL * sms) C *= 2;
-    if ((rc = launch_dependent(fd::fd_select_kernel, dim3(static_cast<unsigned>(rows * C)), fd::kSelectThreads, 0, st, C,
-                               p)) != FD_OK)
-        return rc;
+    while (C < 8 && max_len / C > fd::kShortSlice && static_cast<long long>(rows) * C * 2 <= sms) C *= 2;
+    const dim3 blocks(static_cast<unsigned>(rows * C));
+    rc = max_len <= static_cast<long long>(fd::kShortSlice) * C
+             ? launch_dependent(fd::fd_select_kernel<256>, blocks, 256, 0, st, C, p)
+             : launch_dependent(fd::fd_select_kernel<1024>, blocks, 1024, 0, st, C, p);
+    if (rc != FD_OK) return rc;
     const long long chunks = (static_cast<long long>(out_len) + fd::kGatherTokens - 1) / fd::kGatherTokens;
     const long long total = static_cast<long long>(rows) * chunks;
     const dim3 grid(static_cast<unsigned>(total < 0x7fffffffLL ? total : 0x7fffffffLL));
