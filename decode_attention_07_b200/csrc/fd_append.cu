@@ -117,7 +117,7 @@ __host__ __device__ constexpr int append_group() {
 }
 
 template <int D, int T, bool kE4M3, bool kPaged>
-__global__ void __launch_bounds__(kAppendThreads) fd_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) fd_append_kernel(const AppendParams p) {
     constexpr int kVec = D / 8;                       // 16-byte chunks of a token
     constexpr int kGroup = append_group<D, T>();      // threads of a group
     constexpr int kGroups = kAppendThreads / kGroup;  // heads of a block
