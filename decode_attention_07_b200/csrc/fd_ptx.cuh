@@ -135,6 +135,15 @@ __device__ __forceinline__ uint64_t l2_policy_evict_first() {
     return p;
 }
 
+// 16 zero bytes at a shared-memory address (16-byte aligned).
+__device__ __forceinline__ void st_shared_zero16(uint32_t addr) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+}
+
+// This thread's shared-memory stores before it come before later asynchronous
+// copies into the same place (ordered after them by a barrier).
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ------------------------------------------------ packed / mixed fp32 math --
 // c + a.lo * b.lo, then + a.hi * b.hi: two fused multiply-adds of bf16 pairs
 // into an fp32 sum (each product exact, each step rounded once) -- the same

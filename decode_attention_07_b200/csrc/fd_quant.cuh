@@ -67,7 +67,8 @@
 
 namespace fd {
 
-template <int D, int NT, bool kE4M3, int kTok = 16, bool kBlock = false, bool kPagedScales = false>
+template <int D, int NT, bool kE4M3, int kTok = 16, bool kBlock = false, bool kPagedScales = false,
+          int kCW = kConsumerWarps>
 struct QuantConsumer {
     static constexpr int G = 8 * NT;        // columns held (padded)
     static constexpr int kElemBytes = 1;
@@ -76,6 +77,7 @@ struct QuantConsumer {
     static constexpr int KACC = MB == 1 ? 2 : 1;      // logit accumulators per block
     static constexpr bool kInterleaved = false;
     static constexpr bool kTileHook = kBlock;
+    static constexpr int kWarps = kCW;
     static constexpr int KC = D / 16;       // 16-byte chunks of a token = k-steps of S = m-tiles of O^T
     static constexpr int kRowBytes = D;
     // The reference max lags the running max by at most kLazy (base 2), so
@@ -159,7 +161,7 @@ struct QuantConsumer {
         if constexpr (kPagedScales) {
             fetch_pages(p, c.b, t0, L);
             fetch_scales(p, c, t0, L);
-            fetch_pages(p, c.b, t0 + kTileTokens * (kConsumerWarps * kTok / kTileTokens), L);
+            fetch_pages(p, c.b, t0 + kCW * kTok, L);
         } else {
             fetch_scales(p, c, t0, L);
         }
@@ -175,7 +177,7 @@ struct QuantConsumer {
         }
         fetch_scales(p, c, t_next, L);
         if constexpr (kPagedScales)
-            fetch_pages(p, c.b, t_next < 0 ? -1 : t_next + kTileTokens * (kConsumerWarps * kTok / kTileTokens), L);
+            fetch_pages(p, c.b, t_next < 0 ? -1 : t_next + kCW * kTok, L);
     }
 
     __device__ __forceinline__ void reset() {
@@ -253,8 +255,17 @@ struct QuantConsumer {
             for (int e = 0; e < 2; ++e) colmul[nt][e] = __shfl_sync(0xffffffffu, cm[nt], 4 * (2 * cc + e));
     }
 
-    static __device__ __forceinline__ uint32_t keep_tokens(uint32_t w, int t, int valid) {
-        return w & ((t < valid ? 0x0000ffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u));
+    // The slice's value rows from token `valid` on, past the row's end, may
+    // hold anything (NaN codes): zero them in the tile, once in a row, rather
+    // than test every fragment of every tile. Only this warp reads them; the
+    // fence orders the stores before the copy that fills the stage next.
+    static __device__ __forceinline__ void clear_rows(uint32_t v_smem, int slice, int valid) {
+        const int lane = threadIdx.x & 31;
+        const int first = max(valid, 0) * (kRowBytes / 16), end = kWarpTokens * (kRowBytes / 16);
+        for (int i = first + lane; i < end; i += 32)   // whole rows: the swizzle only moves chunks inside a row
+            st_shared_zero16(v_smem + kWarpTokens * slice * kRowBytes + i * 16);
+        fence_proxy_async();
+        __syncwarp();
     }
 
     // One tile: `slice` = this warp's slice of kWarpTokens tokens (MB blocks
@@ -304,6 +315,7 @@ struct QuantConsumer {
         // exceeds it by more than kLazy; otherwise p = 2^(x - m) directly.
         float x[MB][NT][4];
         bool grow = false;
+        const bool ends = valid - (FD_MAX_GROUP - 1) < kWarpTokens;   // some column's range may end in this slice
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -314,12 +326,14 @@ struct QuantConsumer {
                     if (KACC == 2) acc += s[mb][KACC - 1][nt][e];
                     x[mb][nt][e] = acc * (kBlock ? colmul[nt][e & 1] * ks[mb] : colmul[nt][e & 1]);
                 }
-                // token r of this block is inside column e's causal range when r < valid - 16 mb - shift
-                const int va = valid - 16 * mb - shift[nt][0], vb = valid - 16 * mb - shift[nt][1];
-                if (r0 >= va) x[mb][nt][0] = -INFINITY;
-                if (r0 >= vb) x[mb][nt][1] = -INFINITY;
-                if (r0 + 8 >= va) x[mb][nt][2] = -INFINITY;
-                if (r0 + 8 >= vb) x[mb][nt][3] = -INFINITY;
+                if (ends) {
+                    // token r of this block is inside column e's causal range when r < valid - 16 mb - shift
+                    const int va = valid - 16 * mb - shift[nt][0], vb = valid - 16 * mb - shift[nt][1];
+                    if (r0 >= va) x[mb][nt][0] = -INFINITY;
+                    if (r0 >= vb) x[mb][nt][1] = -INFINITY;
+                    if (r0 + 8 >= va) x[mb][nt][2] = -INFINITY;
+                    if (r0 + 8 >= vb) x[mb][nt][3] = -INFINITY;
+                }
                 float ta = m[nt][0] + kLazy, tb = m[nt][1] + kLazy;
                 if constexpr (kBlock) {   // y = x + lv against its own reference (a zero scale never moves it)
                     ta = fminf(ta, mo[nt][0] + kLazy - lv[mb]);
@@ -405,6 +419,8 @@ struct QuantConsumer {
             }
         }
 
+        if (valid < kWarpTokens) clear_rows(v_smem, slice, valid);
+
         // O^T += V^T P^T, one 16-element chunk of head dims per m-tile, one
         // 16-token k-step per block. ldmatrix.trans of the 8-bit tile read as
         // 16-bit elements gives each thread tokens (2cc, 2cc+1) x head dims
@@ -416,7 +432,6 @@ struct QuantConsumer {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
                 const int lrow = base + 16 * mb + rr + 8 * (mi & 1);
-                const int vmb = valid - 16 * mb;
                 uint32_t a[4];
                 ldsm_x4_trans(v_smem + lrow * kRowBytes + (swz(chunk, lrow) << 4), a[0], a[1], a[2], a[3]);
 #pragma unroll
@@ -425,12 +440,6 @@ struct QuantConsumer {
                     uint32_t A0, A1, A2, A3;
                     widen_t(a[2 * half], A0, A1);
                     widen_t(a[2 * half + 1], A2, A3);
-                    if (vmb < 16) {   // rows past the end may hold anything (NaN codes): zero them
-                        A0 = keep_tokens(A0, 2 * cc, vmb);
-                        A1 = keep_tokens(A1, 2 * cc, vmb);
-                        A2 = keep_tokens(A2, 8 + 2 * cc, vmb);
-                        A3 = keep_tokens(A3, 8 + 2 * cc, vmb);
-                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma_f16_16816(o[nt][2 * pc + half], A0, A1, A2, A3, bh[mb][nt][0], bh[mb][nt][1]);

@@ -55,20 +55,15 @@ namespace fd {
 // type can declare 32 tokens per warp (four groups of two warps).
 constexpr int kGroups = 2;                        // default: consumer groups alternating tiles
 constexpr int kSliceWarps = 4;                    // default: warps per group (16 tokens each)
-constexpr int kConsumerWarps = kGroups * kSliceWarps;
-constexpr int kConsumerThreads = kConsumerWarps * 32;
-constexpr int kProducerWarp = kConsumerWarps;     // warp 8
+constexpr int kConsumerWarps = kGroups * kSliceWarps;   // default: a consumer type can declare another count
 constexpr int kFinisherWarps = 2;                 // warps 9, 10
 constexpr int kFinisherThreads = kFinisherWarps * 32;
-constexpr int kSplitThreads = kConsumerThreads + 32 + kFinisherThreads;
-constexpr int kWorkerThreads = kConsumerThreads + kFinisherThreads;   // all but the producer
 // Paged caches add a second producer, warp 11, that brings the V boxes while
 // warp 8 brings K and the query heads: a TMA copy costs its issuing thread a
 // fixed time, which dominates the small boxes of small pages, and copies from
 // two warps start in parallel.
-constexpr int kVProducerWarp = kProducerWarp + 1 + kFinisherWarps;
-template <bool kPaged>
-constexpr int split_threads() { return kSplitThreads + (kPaged ? 32 : 0); }
+template <bool kPaged, int kWarps = kConsumerWarps>   // kWarps: consumer warps
+constexpr int split_threads() { return (kWarps + 1 + kFinisherWarps + (kPaged ? 1 : 0)) * 32; }
 constexpr int kPendingMax = 4;                    // rows or chunks a block completes (a run cuts at most 2
                                                   // rows; each completed chunk may complete its row)
 constexpr int kBarFinishers = 1, kBarWorkers = 2; // named barrier ids
@@ -167,7 +162,8 @@ __device__ __forceinline__ size_t out_row(const SplitParams &p, int b, int h, in
 }
 
 // E = bytes per cached element: 2 (bf16) or 1 (8-bit codes).
-template <int D, int G, int E = 2, bool kPaged = false>
+// CW = consumer warps, CG = consumer groups taking turns on tiles.
+template <int D, int G, int E = 2, bool kPaged = false, int CW = kConsumerWarps, int CG = kGroups>
 struct SplitConfig {
     static constexpr int kRowBytes = D * E;                                // one token of one head
     static constexpr int kBoxRowBytes = kRowBytes < 128 ? kRowBytes : 128; // a box row = one swizzle span
@@ -178,23 +174,24 @@ struct SplitConfig {
     static constexpr int kQSlotBytes = (G * D * 2 + 1023) / 1024 * 1024;   // query heads of a row (bf16)
     static constexpr int kStageBytes = 2 * kTileBytes + kQSlotBytes;       // multiple of 1024 (swizzle)
     static constexpr int kWarpFloats = merge_warp_floats<D, G>();          // o, m, l of one warp
-    static constexpr int kMergeFloats = kConsumerWarps * kWarpFloats;      // one merge buffer
+    static constexpr int kMergeFloats = CW * kWarpFloats;      // one merge buffer
     static constexpr int kCtrlBytes = 2048;                                // barriers, start info, queue, weights
     static constexpr int kPageBytes = kPageWindow * 4;                     // block-table window (paged)
     static constexpr int kFixedBytes = 1024 + kCtrlBytes + (kPaged ? 2 : 1) * kPageBytes;   // one window per producer
     // 128 KiB of K/V tiles in flight (measured best for bf16: 4 stages at
     // D = 128), as many as fit next to one merge buffer, in whole pairs
     static constexpr int fit_stages(int s) {
-        return s > 2 && kFixedBytes + s * kStageBytes + kMergeFloats * 4 > kSmemLimit ? fit_stages(s - 2) : s;
+        return s > kStep && kFixedBytes + s * kStageBytes + kMergeFloats * 4 > kSmemLimit ? fit_stages(s - kStep) : s;
     }
-    static constexpr int kStages = fit_stages(1024 / kRowBytes);
+    static constexpr int kStep = CG % 2 == 0 ? 2 : CG;
+    static constexpr int kStages = fit_stages((1024 / kRowBytes + kStep - 1) / kStep * kStep);
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kMergeBufs = kFixedBytes + kRingBytes + 2 * kMergeFloats * 4 <= kSmemLimit ? 2 : 1;
     static constexpr int kSmemBytes = kFixedBytes + kRingBytes + kMergeBufs * kMergeFloats * 4;
     // Each consumer group owns whole stages: a stage shared by both groups
     // could be waited on two phases ahead of a tile still in flight, where a
     // parity wait would pass on the older phase.
-    static_assert(kStages % 2 == 0, "stages come in pairs");
+    static_assert(kStages % kStep == 0, "stages come in pairs, or in whole rounds of the groups");
     static_assert(kStageBytes % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
     static_assert(kSmemBytes <= kSmemLimit, "shared memory over the limit");
 };
@@ -460,7 +457,7 @@ __device__ __forceinline__ void take_ticket(const SplitParams &p, StartInfo *inf
 // first one thread per head turns the warps' (m, l) into normalised weights
 // w[head][warp] = 2^(m_w - M) / sum_w' 2^(m_w' - M) l_w' and the log-sum-exp,
 // then every output is sum_w w[head][w] * o_w.
-template <int D, int G, class Bar>
+template <int D, int G, int kConsumerWarps, class Bar>
 __device__ __forceinline__ void merge_warps_and_store(const float *merge, float *weights, const SplitParams &p,
                                                       const Cursor &c, bool whole, size_t slot, int tid,
                                                       int nthreads, Bar bar) {
@@ -520,6 +517,7 @@ struct GroupConsumer {
     static constexpr int kWarpTokens = 16;
     static constexpr bool kInterleaved = kInter;
     static constexpr bool kTileHook = kLogits;
+    static constexpr int kWarps = kConsumerWarps;
 
     float *lg;                          // kLogits: logits of this warp's slice of the tile, [token][lcols]
     int lcols;
@@ -727,6 +725,7 @@ struct HeadConsumer {
     static constexpr int NSUB = kTok / 16;     // 16-token halves
     static_assert(kTok == 16 || kTok == 32, "16 or 32 tokens per warp");
     static constexpr bool kTileHook = kLogits;
+    static constexpr int kWarps = kConsumerWarps;
 
     float *lg;                                 // kLogits: logits of this warp's slice of the tile
     uint4 qw;                                  // q[d0 .. d0+7] of this lane's 16-byte chunk (bf16 pairs)
@@ -893,15 +892,20 @@ struct HeadConsumer {
 
 // ------------------------------------------------------------------ kernel --
 template <int D, class Consumer, bool kFused, bool kPaged = false>
-__global__ void __launch_bounds__(split_threads<kPaged>(), 1)
+__global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
     fd_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_vr,
                     const SplitParams p) {
     constexpr int G = Consumer::G;
-    using Cfg = SplitConfig<D, G, Consumer::kElemBytes, kPaged>;
+    constexpr int kConsumerWarps = Consumer::kWarps;
+    constexpr int kConsumerThreads = kConsumerWarps * 32;
+    constexpr int kProducerWarp = kConsumerWarps;         // then the finishers, then the V producer of paged caches
+    constexpr int kVProducerWarp = kProducerWarp + 1 + kFinisherWarps;
+    constexpr int kWorkerThreads = kConsumerThreads + kFinisherThreads;   // all but the producers
     constexpr int kTok = Consumer::kWarpTokens;          // tokens per consumer warp and tile
     constexpr int kSlices = kTileTokens / kTok;           // warps per consumer group
     constexpr int kGroupsC = kConsumerWarps / kSlices;    // groups taking turns on tiles
+    using Cfg = SplitConfig<D, G, Consumer::kElemBytes, kPaged, kConsumerWarps, kGroupsC>;
     // Each consumer group owns whole stages: a stage shared by two groups could
     // be waited on two phases ahead of a tile still in flight, where a parity
     // wait would pass on the older phase.
@@ -1339,7 +1343,7 @@ __global__ void __launch_bounds__(split_threads<kPaged>(), 1)
             const size_t slot = static_cast<size_t>(blockIdx.x) + static_cast<size_t>(u);
             const int buf = static_cast<int>(segctr % kBufs);
             wait_bounded(&mfull[buf], (segctr / kBufs) & 1u, abort);
-            merge_warps_and_store<D, G>(merge + buf * Cfg::kMergeFloats, weights, p, c, whole, slot, ftid,
+            merge_warps_and_store<D, G, kConsumerWarps>(merge + buf * Cfg::kMergeFloats, weights, p, c, whole, slot, ftid,
                                         kFinisherThreads, [] { named_barrier_sync(kBarFinishers, kFinisherThreads); });
             named_barrier_sync(kBarFinishers, kFinisherThreads);   // every finisher is done with the buffer
             if (lane == 0) mbar_arrive(&mempty[buf]);
@@ -1363,7 +1367,7 @@ __global__ void __launch_bounds__(split_threads<kPaged>(), 1)
         const long long u = static_cast<long long>(last_c.b) * p.Hkv + last_c.h;
         const size_t slot = static_cast<size_t>(blockIdx.x) + static_cast<size_t>(u);
         const int buf = static_cast<int>(info->last_buf);
-        merge_warps_and_store<D, G>(merge + buf * Cfg::kMergeFloats, weights, p, last_c, whole, slot, wtid,
+        merge_warps_and_store<D, G, kConsumerWarps>(merge + buf * Cfg::kMergeFloats, weights, p, last_c, whole, slot, wtid,
                                     kWorkerThreads, workers_sync);
         if (kFused && !whole) {
             workers_sync();   // the stores above, before the ticket
