@@ -30,7 +30,7 @@ struct WeightsParams {
     int B, q_len, Hq, Hkv, g, Lmax, cols, lcols;
 };
 
-// kVec floats of a token's logits per load; lcols is a multiple of kVec.
+// kVec floats.
 template <int kVec>
 __device__ __forceinline__ void load_logits(const float *at, float (&x)[kVec]) {
     if constexpr (kVec == 4) {
@@ -44,42 +44,86 @@ __device__ __forceinline__ void load_logits(const float *at, float (&x)[kVec]) {
     }
 }
 
-template <int kVec>
+// Base-2 log-sum-exp of column col of row (b, h); +inf where the column saw
+// nothing and for padding columns, whose weights 2^(x - inf) are then 0.
+__device__ __forceinline__ float column_lse2(const WeightsParams &p, int b, int h, int col) {
+    if (col >= p.cols) return INFINITY;
+    const int j = col / p.g, i = col - j * p.g;
+    const float ls = __ldcg(p.lse + (static_cast<size_t>(b) * p.q_len + j) * p.Hq + h * p.g + i);
+    return ls == -INFINITY ? INFINITY : ls * kLog2eF;
+}
+
+// A token's logits are kN vectors of kVec floats (kVec * kN = lcols). A warp
+// takes 32 tokens at a time, read as 32 kN consecutive vectors, one per lane
+// and load; where kN is a power of two the kN lanes of a token add up their
+// parts and each lane ends with one token of the 32. (Other kN: a token per
+// lane.) Every load, lengths and log-sum-exps among them, is on its way
+// before the first is used: past the row's end they read the buffers' unused
+// part. Logits are read for the last time here, so the whole lines of them
+// leave L2 without being written to memory.
+template <int kVec, int kN>
 __global__ void __launch_bounds__(kWeightsThreads) fd_weights_kernel(const WeightsParams p) {
-    __shared__ float lse2[FD_MAX_GROUP];   // base-2 log-sum-exp of the row's columns; columns that saw nothing: +inf
+    constexpr bool kSplit = (kN & (kN - 1)) == 0;
+    constexpr int kSteps = kWeightsTokens / kWeightsThreads;      // 32-token steps of a warp
+    constexpr int kBatch = kVec * kN > 8 ? 2 : kSteps;            // steps in flight
     grid_dependents_launch();
     grid_dependency_wait();
     const int u = blockIdx.x, b = u / p.Hkv, h = u - b * p.Hkv;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = clamp_len(__ldcg(p.seqlens + b), p.Lmax);
-    if (static_cast<long long>(blockIdx.y) * kWeightsTokens >= L) return;
-    if (threadIdx.x < FD_MAX_GROUP) {
-        const int col = threadIdx.x;
-        float v = INFINITY;                // 2^(x - inf) = 0: padding columns too
-        if (col < p.cols) {
-            const int j = col / p.g, i = col - j * p.g;
-            const float ls = __ldcg(p.lse + (static_cast<size_t>(b) * p.q_len + j) * p.Hq + h * p.g + i);
-            if (ls != -INFINITY) v = ls * kLog2eF;
-        }
-        lse2[col] = v;
-    }
-    __syncthreads();
+    const int part = kSplit ? lane % kN : 0;
+    float lse2[kSplit ? kVec : kVec * kN];
+#pragma unroll
+    for (int k = 0; k < (kSplit ? kVec : kVec * kN); ++k) lse2[k] = column_lse2(p, b, h, part * kVec + k);
     const size_t row = static_cast<size_t>(u) * p.Lmax;
+    // the lane's token among a step's 32
+    const int mine = kSplit ? part * (32 / kN) + lane / kN : lane;
     for (long long t0 = static_cast<long long>(blockIdx.y) * kWeightsTokens; t0 < L;
          t0 += static_cast<long long>(gridDim.y) * kWeightsTokens) {
 #pragma unroll
-        for (int i = 0; i < kWeightsTokens / kWeightsThreads; ++i) {
-            const long long t = t0 + i * kWeightsThreads + threadIdx.x;
-            if (t >= L) break;
-            const size_t at = row + static_cast<size_t>(t);
-            float w = p.w_in ? __ldcg(p.w_in + at) : 0.f;
-            float sum = 0.f;
-            for (int c = 0; c < p.lcols; c += kVec) {
-                float x[kVec];
-                load_logits<kVec>(p.logits + at * p.lcols + c, x);
+        for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+            float x[kBatch][kN][kVec], w[kBatch];
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) sum += ex2(x[k] - lse2[c + k]);
+            for (int s = 0; s < kBatch; ++s) {
+                const long long t = t0 + (s0 + s) * kWeightsThreads + warp * 32;
+#pragma unroll
+                for (int j = 0; j < kN; ++j) {
+                    const int tok = kSplit ? (j * 32 + lane) / kN : lane;
+                    const int off = kSplit ? (j * 32 + lane) * kVec : (lane * kN + j) * kVec;
+                    if (t + tok < p.Lmax)
+                        load_logits<kVec>(p.logits + (row + t) * (kVec * kN) + off, x[s][j]);
+                    else
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) x[s][j][k] = -INFINITY;
+                }
+                w[s] = p.w_in && t + mine < p.Lmax ? __ldcg(p.w_in + row + t + mine) : 0.f;
             }
-            p.w_out[at] = w + sum;
+#pragma unroll
+            for (int s = 0; s < kBatch; ++s) {
+                const long long t = t0 + (s0 + s) * kWeightsThreads + warp * 32;
+                float sum = 0.f;
+                if constexpr (kSplit) {
+#pragma unroll
+                    for (int j = 0; j < kN; ++j) {
+                        float v = 0.f;
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) v += ex2(x[s][j][k] - lse2[k]);
+#pragma unroll
+                        for (int sh = 1; sh < kN; sh <<= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
+                        sum = j == part ? v : sum;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kN; ++j)
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) sum += ex2(x[s][j][k] - lse2[j * kVec + k]);
+                }
+                if (t + mine < L) p.w_out[row + t + mine] = w[s] + sum;
+                __syncwarp();   // every lane has its logits
+                const float *lines = p.logits + (row + t) * (kVec * kN);
+                if (lane < kVec * kN && t + 32 <= p.Lmax && (reinterpret_cast<uintptr_t>(lines) & 127) == 0)
+                    discard_l2_128(lines + lane * 32);
+            }
         }
     }
 }
@@ -109,6 +153,11 @@ int launch_logits(int D, bool rows_map, const CUtensorMap &tk, const CUtensorMap
     if (p.cols == 1) return launch_split_t<64, fd::HeadConsumer<64, false, 16, true>, true, false>(tk, tv, p, st);
     if (p.cols <= 8) return launch_split_t<64, fd::GroupConsumer<64, 1, false, true>, true, false>(tk, tv, p, st);
     return launch_split_t<64, fd::GroupConsumer<64, 2, false, true>, true, false>(tk, tv, p, st);
+}
+
+template <int kVec, int kN>
+int launch_weights(dim3 grid, const fd::WeightsParams &w, cudaStream_t st) {
+    return launch_dependent(fd::fd_weights_kernel<kVec, kN>, grid, fd::kWeightsThreads, 0, st, 1, w);
 }
 
 int check_weights_shape(int B, int q_len, int Hq, int Hkv, int D, int max_len) {
@@ -200,9 +249,17 @@ int fd_decode_weights(int B, int q_len, int Hq, int Hkv, int D, int max_len, con
     w.lcols = fd::logit_cols(cols);
     const long long chunks = (static_cast<long long>(max_len) + fd::kWeightsTokens - 1) / fd::kWeightsTokens;
     const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(chunks < 65535 ? chunks : 65535));
-    if (w.lcols % 4 == 0) return launch_dependent(fd::fd_weights_kernel<4>, grid, fd::kWeightsThreads, 0, pr.stream, 1, w);
-    if (w.lcols % 2 == 0) return launch_dependent(fd::fd_weights_kernel<2>, grid, fd::kWeightsThreads, 0, pr.stream, 1, w);
-    return launch_dependent(fd::fd_weights_kernel<1>, grid, fd::kWeightsThreads, 0, pr.stream, 1, w);
+    switch (w.lcols) {
+        case 1: return launch_weights<1, 1>(grid, w, pr.stream);
+        case 2: return launch_weights<2, 1>(grid, w, pr.stream);
+        case 4: return launch_weights<4, 1>(grid, w, pr.stream);
+        case 6: return launch_weights<2, 3>(grid, w, pr.stream);
+        case 8: return launch_weights<4, 2>(grid, w, pr.stream);
+        case 10: return launch_weights<2, 5>(grid, w, pr.stream);
+        case 12: return launch_weights<4, 3>(grid, w, pr.stream);
+        case 14: return launch_weights<2, 7>(grid, w, pr.stream);
+        default: return launch_weights<4, 4>(grid, w, pr.stream);
+    }
 }
 
 }  // extern "C"
