@@ -57,24 +57,30 @@ __device__ __forceinline__ float column_lse2(const WeightsParams &p, int b, int 
 // takes 32 tokens at a time, read as 32 kN consecutive vectors, one per lane
 // and load; where kN is a power of two the kN lanes of a token add up their
 // parts and each lane ends with one token of the 32. (Other kN: a token per
-// lane.) Every load, lengths and log-sum-exps among them, is on its way
-// before the first is used: past the row's end they read the buffers' unused
-// part. Logits are read for the last time here, so the whole lines of them
-// leave L2 without being written to memory.
+// lane.) All of a step's loads are on their way before the first is used
+// (between seqlens and the buffers' end they read the unused part). The
+// log-sum-exps are read by one warp per block: every block of a row wants the
+// same 64 bytes, and asking for them from every warp kept one L2 slice busy
+// for 7 us of 15 on a row of 131072 tokens. Logits are read for the last
+// time here, so the whole lines of them leave L2 without being written to
+// memory (33 MB a call at 64 heads over 131072 tokens: 107 -> 101 us).
 template <int kVec, int kN>
 __global__ void __launch_bounds__(kWeightsThreads) fd_weights_kernel(const WeightsParams p) {
     constexpr bool kSplit = (kN & (kN - 1)) == 0;
     constexpr int kSteps = kWeightsTokens / kWeightsThreads;      // 32-token steps of a warp
     constexpr int kBatch = kVec * kN > 8 ? 2 : kSteps;            // steps in flight
+    __shared__ float lse2_of[FD_MAX_GROUP];
     grid_dependents_launch();
     grid_dependency_wait();
     const int u = blockIdx.x, b = u / p.Hkv, h = u - b * p.Hkv;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = clamp_len(__ldcg(p.seqlens + b), p.Lmax);
+    if (static_cast<long long>(blockIdx.y) * kWeightsTokens >= L) return;
+    float column = 0.f;
+    if (threadIdx.x < FD_MAX_GROUP) column = column_lse2(p, b, h, threadIdx.x);
+    bool have_lse2 = false;
     const int part = kSplit ? lane % kN : 0;
     float lse2[kSplit ? kVec : kVec * kN];
-#pragma unroll
-    for (int k = 0; k < (kSplit ? kVec : kVec * kN); ++k) lse2[k] = column_lse2(p, b, h, part * kVec + k);
     const size_t row = static_cast<size_t>(u) * p.Lmax;
     // the lane's token among a step's 32
     const int mine = kSplit ? part * (32 / kN) + lane / kN : lane;
@@ -97,6 +103,13 @@ __global__ void __launch_bounds__(kWeightsThreads) fd_weights_kernel(const Weigh
                         for (int k = 0; k < kVec; ++k) x[s][j][k] = -INFINITY;
                 }
                 w[s] = p.w_in && t + mine < p.Lmax ? __ldcg(p.w_in + row + t + mine) : 0.f;
+            }
+            if (!have_lse2) {   // once, with the first step's loads on their way
+                if (threadIdx.x < FD_MAX_GROUP) lse2_of[threadIdx.x] = column;
+                __syncthreads();
+#pragma unroll
+                for (int k = 0; k < (kSplit ? kVec : kVec * kN); ++k) lse2[k] = lse2_of[part * kVec + k];
+                have_lse2 = true;
             }
 #pragma unroll
             for (int s = 0; s < kBatch; ++s) {
