@@ -1099,6 +1099,71 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
             *page = win[lp - win_lo];
             return true;
         };
+        // Pages of 64 tokens or more: every tile lies in one page. A loop of its
+        // own, short enough that one thread keeps up (through the general loop
+        // below a tile costs it 830 cycles, an SM's share of the memory
+        // bandwidth 640): the page is looked up before the wait for the stage,
+        // coordinates advance with the tile.
+        if (kPaged && p.page_shift >= 6) {
+            uint32_t stage = 0, phase = 0, seq = 0;
+            if (restart) seq = kStages, phase = 1;
+            const CUtensorMap *map = v_role ? &tm_v : &tm_k;
+            const int in_page = (1 << p.page_shift) - 1;
+            while (remaining > 0) {
+                const int seg = static_cast<int>(min(static_cast<long long>(c.n - c.tile), remaining));
+                int page = 0, have = -1;   // `page` of logical page `have`
+                for (int k = 0; k < seg; ++k, ++seq) {
+                    const int y = (c.tile + k) * kTileTokens, lp = y >> p.page_shift;
+                    if (lp != have) {
+                        if (!page_of(c.b, lp, &page)) {
+                            drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+                            return;
+                        }
+                        have = lp;
+                        // a page outside the pool gets a coordinate outside the tensor (zeros)
+                        if (page < 0 || page >= p.num_pages)
+                            page = -kTileTokens - in_page;
+                        else
+                            page = p.kv_nhd ? page << p.page_shift : page * p.Hkv + c.h;
+                    }
+                    const int off = y & in_page;
+                    const int cy = p.kv_nhd ? c.h : off, cz = p.kv_nhd ? page + off : page;
+                    if (*abort || !wait_bounded(&empty[stage], phase ^ 1u, abort)) {
+                        drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+                        return;
+                    }
+                    uint8_t *dst = ring + stage * Cfg::kStageBytes + (v_role ? Cfg::kTileBytes : 0);
+                    const bool with_q = k < kGroupsC && !v_role;   // each group's first tile of the segment
+                    mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes + (with_q ? q_bytes : 0u));
+#ifdef FD_DEBUG
+                    const bool withhold = blockIdx.x == 0 && static_cast<int>(seq) == p.debug_withhold;   // armed, never filled
+#else
+                    constexpr bool withhold = false;
+#endif
+                    if (!withhold) {
+#pragma unroll
+                        for (int bx = 0; bx < Cfg::kBoxes; ++bx)
+                            tma_load_3d(dst + bx * Cfg::kBoxBytes, map, &full[stage], Cfg::kBoxCols * bx, cy, cz, policy);
+                        if (with_q) {
+                            const uint16_t *q_row = p.q + (static_cast<size_t>(c.b) * p.q_len * p.Hq +
+                                                           static_cast<size_t>(c.h) * p.g) * D;
+                            const uint32_t q_run = static_cast<uint32_t>(p.g) * D * 2;
+                            for (int j = 0; j < p.q_len; ++j) {
+                                const uint16_t *src = q_row + static_cast<size_t>(j) * p.Hq * D;
+                                if (FD_DCHECK(src >= p.q && src + q_run / 2 <= p.q + out_rows(p) * D))
+                                    bulk_load(ring + stage * Cfg::kStageBytes + 2 * Cfg::kTileBytes + j * q_run, src, q_run,
+                                              &full[stage]);
+                            }
+                        }
+                    }
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
+                remaining -= seg;
+                if (remaining > 0) next_row(c, p);
+            }
+            if (*abort) drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+            return;
+        }
         // without a restart the guessed tiles already issued are the real first
         // ones: skip them below; after a restart, go on from kStages
         uint32_t seq = restart ? kStages : 0, skip = restart ? 0 : n_spec;
