@@ -16,7 +16,8 @@
 //               TMA loads, 128-byte swizzled, mbarrier completion; with each
 //               group's first tile of a row segment it also bulk-copies that
 //               row's query heads into the stage. Paged caches: it brings K
-//               and the query heads, and warp 11 (one lane) brings V.
+//               and the query heads, and warp 11 (one lane) brings V; with
+//               pages of 64 tokens or more the two take alternate tiles.
 //   warps 0..7  consumers in two groups of four. Group q takes the tiles with
 //               sequence number = q (mod 2), so each SM sub-partition runs two
 //               independent chains; warp w of a group owns tokens
@@ -262,11 +263,12 @@ __device__ __forceinline__ void drain_phase(uint64_t *bar, uint32_t parity) {
 
 // The producer's copies still possibly in flight when it gives up: the last
 // load issued into each stage (`issued` tiles so far, stage = tile % stages)
-// and the block-table window (when `window_pending`).
+// and the block-table window (when `window_pending`). A producer that owns
+// every step-th stage from `first` on drains those.
 template <int kStages>
 __device__ __forceinline__ void drain_copies(uint64_t *full, uint32_t issued, uint64_t *pbar, bool window_pending,
-                                             uint32_t win_phase) {
-    for (uint32_t s = 0; s < static_cast<uint32_t>(kStages) && s < issued; ++s) {
+                                             uint32_t win_phase, uint32_t first = 0, uint32_t step = 1) {
+    for (uint32_t s = first; s < static_cast<uint32_t>(kStages) && s < issued; s += step) {
         const uint32_t n = (issued - 1 - s) / kStages + 1;   // loads issued into stage s
         drain_phase(&full[s], (n - 1) & 1u);
     }
@@ -486,22 +488,31 @@ __device__ __forceinline__ void merge_warps_and_store(const float *merge, float 
         }
     }
     bar();
-    for (int idx = tid; idx < p.cols * D; idx += nthreads) {
-        const int head = idx / D, d = idx - head * D;
-        float o = 0.f;
+    // four outputs per thread and step: a short row's merge is on the path of
+    // the block that holds many of them (two warps merge while the consumers
+    // go on)
+    for (int idx = tid; idx < p.cols * (D / 4); idx += nthreads) {
+        const int head = idx / (D / 4), d4 = idx - head * (D / 4);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kConsumerWarps; ++w)
-            o = fmaf(weights[head * kConsumerWarps + w], merge[w * kWarpFloats + head * S + d], o);
+        for (int w = 0; w < kConsumerWarps; ++w) {
+            const float wt = weights[head * kConsumerWarps + w];
+            const float4 v = reinterpret_cast<const float4 *>(merge + w * kWarpFloats + head * S)[d4];
+            o.x = fmaf(wt, v.x, o.x);
+            o.y = fmaf(wt, v.y, o.y);
+            o.z = fmaf(wt, v.z, o.z);
+            o.w = fmaf(wt, v.w, o.w);
+        }
         if (whole) {
             const size_t row = out_row(p, c.b, c.h, head);
             if (!FD_DCHECK(row < out_rows(p))) continue;
-            p.out[row * D + d] = o;
-            if (d == 0) p.lse[row] = lse_h[head];
+            reinterpret_cast<float4 *>(p.out + row * D)[d4] = o;
+            if (d4 == 0) p.lse[row] = lse_h[head];
         } else {
             const size_t row = slot * p.cols + head;
             if (!FD_DCHECK(row < seg_rows(p))) continue;
-            p.seg_out[row * D + d] = o;
-            if (d == 0) p.seg_lse[row] = lse_h[head];
+            reinterpret_cast<float4 *>(p.seg_out + row * D)[d4] = o;
+            if (d4 == 0) p.seg_lse[row] = lse_h[head];
         }
     }
 }
@@ -947,7 +958,8 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], kPaged ? 2 : 1);   // paged caches: the K and the V producer arrive
+            // paged caches with pages below a tile: the K and the V producer arrive
+            mbar_init(&full[s], kPaged && p.page_shift < 6 ? 2 : 1);
             mbar_init(&empty[s], kSlices);
         }
         for (int b = 0; b < kBufs; ++b) {
@@ -1066,7 +1078,8 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
     volatile int *abort = &info->abort;
     const uint32_t q_bytes = static_cast<uint32_t>(p.cols) * D * 2;   // q_len copies of g rows
 
-    // paged caches: warp 8 brings K and the query heads, warp 11 brings V
+    // paged caches: warp 8 brings K and the query heads, warp 11 brings V (pages of
+    // 64 tokens or more: they take alternate tiles)
     const bool v_role = kPaged && warp == kVProducerWarp;
     if (warp == kProducerWarp || v_role) {
         // ---------------------------------------------------- producer --
@@ -1099,24 +1112,27 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
             *page = win[lp - win_lo];
             return true;
         };
-        // Pages of 64 tokens or more: every tile lies in one page. A loop of its
-        // own, short enough that one thread keeps up (through the general loop
-        // below a tile costs it 830 cycles, an SM's share of the memory
-        // bandwidth 640): the page is looked up before the wait for the stage,
-        // coordinates advance with the tile.
+        // Pages of 64 tokens or more: every tile lies in one page. The two
+        // producer warps take alternate tiles (and so alternate stages), K and
+        // V of a tile from one thread, in a loop of its own: a tile costs its
+        // thread a page lookup, a wait and the copies, and an SM's share of
+        // the memory bandwidth is a tile of 8-bit codes every 640 cycles
+        // (the general loop below, K and V apart, takes 830 cycles a tile,
+        // this loop's arithmetic with K and V apart 670).
         if (kPaged && p.page_shift >= 6) {
-            uint32_t stage = 0, phase = 0, seq = 0;
+            static_assert(kStages % 2 == 0, "each producer owns whole stages");
+            const uint32_t role = v_role ? 1 : 0;
+            uint32_t stage = role, phase = 0, seq = 0;
             if (restart) seq = kStages, phase = 1;
-            const CUtensorMap *map = v_role ? &tm_v : &tm_k;
             const int in_page = (1 << p.page_shift) - 1;
             while (remaining > 0) {
                 const int seg = static_cast<int>(min(static_cast<long long>(c.n - c.tile), remaining));
                 int page = 0, have = -1;   // `page` of logical page `have`
-                for (int k = 0; k < seg; ++k, ++seq) {
+                for (int k = static_cast<int>((role - seq) & 1u); k < seg; k += 2) {
                     const int y = (c.tile + k) * kTileTokens, lp = y >> p.page_shift;
                     if (lp != have) {
                         if (!page_of(c.b, lp, &page)) {
-                            drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+                            drain_copies<kStages>(full, seq + k, wbar, win_pending, win_phase, role, 2);
                             return;
                         }
                         have = lp;
@@ -1129,21 +1145,19 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                     const int off = y & in_page;
                     const int cy = p.kv_nhd ? c.h : off, cz = p.kv_nhd ? page + off : page;
                     if (*abort || !wait_bounded(&empty[stage], phase ^ 1u, abort)) {
-                        drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+                        drain_copies<kStages>(full, seq + k, wbar, win_pending, win_phase, role, 2);
                         return;
                     }
-                    uint8_t *dst = ring + stage * Cfg::kStageBytes + (v_role ? Cfg::kTileBytes : 0);
-                    const bool with_q = k < kGroupsC && !v_role;   // each group's first tile of the segment
-                    mbar_arrive_expect_tx(&full[stage], Cfg::kTileBytes + (with_q ? q_bytes : 0u));
+                    uint8_t *dst = ring + stage * Cfg::kStageBytes;
+                    const bool with_q = k < kGroupsC;   // each group's first tile of the segment
+                    mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTileBytes + (with_q ? q_bytes : 0u));
 #ifdef FD_DEBUG
-                    const bool withhold = blockIdx.x == 0 && static_cast<int>(seq) == p.debug_withhold;   // armed, never filled
+                    const bool withhold = blockIdx.x == 0 && static_cast<int>(seq + k) == p.debug_withhold;   // armed, never filled
 #else
                     constexpr bool withhold = false;
 #endif
                     if (!withhold) {
-#pragma unroll
-                        for (int bx = 0; bx < Cfg::kBoxes; ++bx)
-                            tma_load_3d(dst + bx * Cfg::kBoxBytes, map, &full[stage], Cfg::kBoxCols * bx, cy, cz, policy);
+                        load_tile<Cfg, false>(dst, dst + Cfg::kTileBytes, &tm_k, &tm_v, &full[stage], cy, cz, policy);
                         if (with_q) {
                             const uint16_t *q_row = p.q + (static_cast<size_t>(c.b) * p.q_len * p.Hq +
                                                            static_cast<size_t>(c.h) * p.g) * D;
@@ -1151,17 +1165,18 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                             for (int j = 0; j < p.q_len; ++j) {
                                 const uint16_t *src = q_row + static_cast<size_t>(j) * p.Hq * D;
                                 if (FD_DCHECK(src >= p.q && src + q_run / 2 <= p.q + out_rows(p) * D))
-                                    bulk_load(ring + stage * Cfg::kStageBytes + 2 * Cfg::kTileBytes + j * q_run, src, q_run,
-                                              &full[stage]);
+                                    bulk_load(dst + 2 * Cfg::kTileBytes + j * q_run, src, q_run, &full[stage]);
                             }
                         }
                     }
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                    stage += 2;
+                    if (stage >= kStages) stage -= kStages, phase ^= 1u;
                 }
+                seq += static_cast<uint32_t>(seg);
                 remaining -= seg;
                 if (remaining > 0) next_row(c, p);
             }
-            if (*abort) drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
+            if (*abort) drain_copies<kStages>(full, seq, wbar, win_pending, win_phase, role, 2);
             return;
         }
         // without a restart the guessed tiles already issued are the real first
