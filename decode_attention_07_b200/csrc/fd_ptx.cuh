@@ -176,6 +176,16 @@ __device__ __forceinline__ void fma_f32x2_bf16(float &c0, float &c1, float a, ui
         : "f"(a), "r"(w));
 }
 
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1): two fp32 fused multiply-adds in
+// one packed instruction.
+__device__ __forceinline__ void fma2(float a0, float a1, float b0, float b1, float c0, float c1, float &d0, float &d1) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
 // --------------------------------------------------------- tensor-core ops --
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {

@@ -51,13 +51,15 @@
 //     x_t = scale log2(e) k_scale[t / T] (q . decode(k_t)),
 //     out = sum_t 2^(x_t - m) v_scale[t / T] decode(v_t) / sum_t 2^(x_t - m).
 //   * The key scale multiplies the block's logits. The value scale joins the
-//     weight's exponent: with y_t = x_t + log2 v_scale[t / T], P V takes
-//     2^(y_t - mo) and the sum 2^(x_t - m), each with a lazy reference maximum
-//     of its own, both moved by the same rare branch. So whatever the scales'
-//     spread, P keeps its f16 range relative to the row's largest
-//     contribution; a zero scale gives y = -inf, weight 0. This costs a second
-//     2^x per (token, column), 4 of about 200 issue slots a thread spends on
-//     a tile at up to 8 columns.
+//     weight: with y_t = x_t + log2 v_scale[t / T], P V takes 2^(y_t - mo) and
+//     the sum 2^(x_t - m), each with a lazy reference maximum of its own, both
+//     moved by the same rare branch. So P keeps its f16 range relative to the
+//     row's largest contribution, not to its largest scale; a zero scale gives
+//     weight 0.
+//   * Consumers are what bounds it next to memory (two consumer warps per
+//     scheduler issue 0.6 instructions a cycle), so the arithmetic counts:
+//     p = 2^(fma(q.k, c, kPScale - m)) and one factor per (block, column) for
+//     the values; the test for a new reference looks at the p themselves.
 //   * A warp reads its 16-token blocks' scales (through the block table for
 //     paged caches) one tile of its group ahead, with loads from L2, so their
 //     latency lies behind a tile's arithmetic.
@@ -183,9 +185,9 @@ struct QuantConsumer {
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = kBlock ? kNoRef : -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
-            if constexpr (kBlock) mo[nt][0] = mo[nt][1] = -INFINITY;
+            if constexpr (kBlock) mo[nt][0] = mo[nt][1] = kNoRef;
 #pragma unroll
             for (int c = 0; c < KC; ++c) o[nt][c][0] = o[nt][c][1] = o[nt][c][2] = o[nt][c][3] = 0.f;
         }
@@ -268,35 +270,35 @@ struct QuantConsumer {
         __syncwarp();
     }
 
-    // One tile: `slice` = this warp's slice of kWarpTokens tokens (MB blocks
-    // of 16), `valid` = how many of those tokens are inside the row.
-    __device__ __forceinline__ void tile(uint32_t k_smem, uint32_t v_smem, int slice, int valid, float) {
-        const int lane = threadIdx.x & 31;
-        const int mi = lane >> 3, rr = lane & 7;
-        const int r0 = lane >> 2, cc = lane & 3;
-        const int base = kWarpTokens * slice;
+    // This lane's ldmatrix address in a tile at `smem`: row 16 (block) + rr +
+    // 8 (mi & 1), chunk mi >> 1, of matrix mi = lane / 8. Chunk pair pc is at
+    // that address ^ (pc << 5): the swizzle xors chunk bits with row bits, and
+    // tiles are 1024-byte aligned.
+    static __device__ __forceinline__ uint32_t lane_addr(uint32_t smem, int slice) {
+        const int lane = threadIdx.x & 31, mi = lane >> 3;
+        const int row = kWarpTokens * slice + (lane & 7) + 8 * (mi & 1);
+        return smem + row * kRowBytes + (swz(mi >> 1, row) << 4);
+    }
 
-        // logits S^T = K Q^T per 16-token block; ldmatrix x4 over two chunks:
-        // matrices (tokens 0-7 | 8-15) x (chunk 2pc | 2pc+1). One block keeps
-        // two accumulators (even / odd chunks) for two independent mma
-        // chains; two blocks already give two.
-        float s[MB][KACC][NT][4];
+    // Logits S^T = K Q^T per 16-token block; ldmatrix x4 over two chunks:
+    // matrices (tokens 0-7 | 8-15) x (chunk 2pc | 2pc+1). One block keeps
+    // two accumulators (even / odd chunks) for two independent mma
+    // chains; two blocks already give two.
+    __device__ __forceinline__ void logits(uint32_t k_smem, int slice, float (&s)[MB][NT][4]) {
+        float s2[MB][NT][4];
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-            for (int a = 0; a < KACC; ++a)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mb][a][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[mb][nt][e] = s2[mb][nt][e] = 0.f;
+        const uint32_t addr = lane_addr(k_smem, slice);
 #pragma unroll
         for (int pc = 0; pc < KC / 2; ++pc) {
-            const int chunk = 2 * pc + (mi >> 1);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                const int lrow = base + 16 * mb + rr + 8 * (mi & 1);
                 uint32_t a0, a1, a2, a3;
-                ldsm_x4(k_smem + lrow * kRowBytes + (swz(chunk, lrow) << 4), a0, a1, a2, a3);
+                ldsm_x4((addr ^ (pc << 5)) + mb * 16 * kRowBytes, a0, a1, a2, a3);
                 uint32_t l0, h0, l1, h1, l2, h2, l3, h3;
                 widen(a0, l0, h0);
                 widen(a1, l1, h1);
@@ -304,136 +306,47 @@ struct QuantConsumer {
                 widen(a3, l3, h3);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16_16816(s[mb][0][nt], l0, l1, h0, h1, qf[nt][2 * pc][0], qf[nt][2 * pc][1]);
-                    mma_f16_16816(s[mb][KACC - 1][nt], l2, l3, h2, h3, qf[nt][2 * pc + 1][0], qf[nt][2 * pc + 1][1]);
+                    mma_f16_16816(s[mb][nt], l0, l1, h0, h1, qf[nt][2 * pc][0], qf[nt][2 * pc][1]);
+                    mma_f16_16816(KACC == 2 ? s2[mb][nt] : s[mb][nt], l2, l3, h2, h3, qf[nt][2 * pc + 1][0],
+                                  qf[nt][2 * pc + 1][1]);
                 }
             }
         }
+        if (KACC == 2)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mb][nt][e] += s2[mb][nt][e];
+    }
 
-        // Online softmax per column with a lazy reference maximum: m moves
-        // (and the accumulators are rescaled) only when a logit of the tile
-        // exceeds it by more than kLazy; otherwise p = 2^(x - m) directly.
-        float x[MB][NT][4];
-        bool grow = false;
-        const bool ends = valid - (FD_MAX_GROUP - 1) < kWarpTokens;   // some column's range may end in this slice
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float acc = s[mb][0][nt][e];
-                    if (KACC == 2) acc += s[mb][KACC - 1][nt][e];
-                    x[mb][nt][e] = acc * (kBlock ? colmul[nt][e & 1] * ks[mb] : colmul[nt][e & 1]);
-                }
-                if (ends) {
-                    // token r of this block is inside column e's causal range when r < valid - 16 mb - shift
-                    const int va = valid - 16 * mb - shift[nt][0], vb = valid - 16 * mb - shift[nt][1];
-                    if (r0 >= va) x[mb][nt][0] = -INFINITY;
-                    if (r0 >= vb) x[mb][nt][1] = -INFINITY;
-                    if (r0 + 8 >= va) x[mb][nt][2] = -INFINITY;
-                    if (r0 + 8 >= vb) x[mb][nt][3] = -INFINITY;
-                }
-                float ta = m[nt][0] + kLazy, tb = m[nt][1] + kLazy;
-                if constexpr (kBlock) {   // y = x + lv against its own reference (a zero scale never moves it)
-                    ta = fminf(ta, mo[nt][0] + kLazy - lv[mb]);
-                    tb = fminf(tb, mo[nt][1] + kLazy - lv[mb]);
-                }
-                grow |= x[mb][nt][0] > ta || x[mb][nt][2] > ta || x[mb][nt][1] > tb || x[mb][nt][3] > tb;
-            }
-        if (__any_sync(0xffffffffu, grow)) {   // the fallback: a synchronised rescale
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float ma = -INFINITY, mbx = -INFINITY;
-                float ya = -INFINITY, yb = -INFINITY;   // kBlock: the same of y
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    const float xa = fmaxf(x[mb][nt][0], x[mb][nt][2]), xb = fmaxf(x[mb][nt][1], x[mb][nt][3]);
-                    ma = fmaxf(ma, xa);
-                    mbx = fmaxf(mbx, xb);
-                    if constexpr (kBlock) {
-                        ya = fmaxf(ya, xa + lv[mb]);
-                        yb = fmaxf(yb, xb + lv[mb]);
-                    }
-                }
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) {
-                    ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
-                    mbx = fmaxf(mbx, __shfl_xor_sync(0xffffffffu, mbx, sh));
-                    if constexpr (kBlock) {
-                        ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, sh));
-                        yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, sh));
-                    }
-                }
-                const float na = fmaxf(m[nt][0], ma), nb = fmaxf(m[nt][1], mbx);
-                const float ua = na == -INFINITY ? 0.f : na, ub = nb == -INFINITY ? 0.f : nb;
-                float alpha_a = ex2(m[nt][0] - ua), alpha_b = ex2(m[nt][1] - ub);
-                l[nt][0] *= alpha_a;
-                l[nt][1] *= alpha_b;
-                m[nt][0] = na;
-                m[nt][1] = nb;
-                if constexpr (kBlock) {   // the accumulators go by y's reference
-                    const float oa = fmaxf(mo[nt][0], ya), ob = fmaxf(mo[nt][1], yb);
-                    alpha_a = ex2(mo[nt][0] - (oa == -INFINITY ? 0.f : oa));
-                    alpha_b = ex2(mo[nt][1] - (ob == -INFINITY ? 0.f : ob));
-                    mo[nt][0] = oa;
-                    mo[nt][1] = ob;
-                }
-#pragma unroll
-                for (int c = 0; c < KC; ++c) {
-                    o[nt][c][0] *= alpha_a;
-                    o[nt][c][1] *= alpha_b;
-                    o[nt][c][2] *= alpha_a;
-                    o[nt][c][3] *= alpha_b;
-                }
-            }
-        }
+    // P^T fragments of one block and n-tile (f16 high part + remainder).
+    static __device__ __forceinline__ void split_p(float p0, float p1, float p2, float p3, uint32_t (&bh)[2],
+                                                   uint32_t (&bl)[2]) {
+        const uint32_t h01 = pack_f16x2(p0, p1), h23 = pack_f16x2(p2, p3);
+        const uint32_t l01 = pack_f16x2(p0 - f16lo_to_f32(h01), p1 - f16hi_to_f32(h01));
+        const uint32_t l23 = pack_f16x2(p2 - f16lo_to_f32(h23), p3 - f16hi_to_f32(h23));
+        bh[0] = movmatrix_trans(h01);
+        bh[1] = movmatrix_trans(h23);
+        bl[0] = movmatrix_trans(l01);
+        bl[1] = movmatrix_trans(l23);
+    }
 
-        // P^T fragments per block (f16 high part + remainder, x 2^kPScale)
-        uint32_t bh[MB][NT][2], bl[MB][NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float ta = kPScale - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
-            float tb = kPScale - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb) {
-                float p0 = ex2(x[mb][nt][0] + ta), p2 = ex2(x[mb][nt][2] + ta);
-                float p1 = ex2(x[mb][nt][1] + tb), p3 = ex2(x[mb][nt][3] + tb);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                if constexpr (kBlock) {   // P V's weights: 2^(y - mo), with the same 2^kPScale
-                    const float ya = kPScale + lv[mb] - (mo[nt][0] == -INFINITY ? 0.f : mo[nt][0]);
-                    const float yb = kPScale + lv[mb] - (mo[nt][1] == -INFINITY ? 0.f : mo[nt][1]);
-                    p0 = ex2(x[mb][nt][0] + ya);
-                    p2 = ex2(x[mb][nt][2] + ya);
-                    p1 = ex2(x[mb][nt][1] + yb);
-                    p3 = ex2(x[mb][nt][3] + yb);
-                }
-                const uint32_t h01 = pack_f16x2(p0, p1), h23 = pack_f16x2(p2, p3);
-                const uint32_t l01 = pack_f16x2(p0 - f16lo_to_f32(h01), p1 - f16hi_to_f32(h01));
-                const uint32_t l23 = pack_f16x2(p2 - f16lo_to_f32(h23), p3 - f16hi_to_f32(h23));
-                bh[mb][nt][0] = movmatrix_trans(h01);
-                bh[mb][nt][1] = movmatrix_trans(h23);
-                bl[mb][nt][0] = movmatrix_trans(l01);
-                bl[mb][nt][1] = movmatrix_trans(l23);
-            }
-        }
-
-        if (valid < kWarpTokens) clear_rows(v_smem, slice, valid);
-
-        // O^T += V^T P^T, one 16-element chunk of head dims per m-tile, one
-        // 16-token k-step per block. ldmatrix.trans of the 8-bit tile read as
-        // 16-bit elements gives each thread tokens (2cc, 2cc+1) x head dims
-        // (2r0, 2r0+1) of a chunk; the widening regroups them into token pairs
-        // at head dims 2r0 (accumulator row r0) and 2r0 + 1 (row r0 + 8).
+    // O^T += V^T P^T, one 16-element chunk of head dims per m-tile, one
+    // 16-token k-step per block. ldmatrix.trans of the 8-bit tile read as
+    // 16-bit elements gives each thread tokens (2cc, 2cc+1) x head dims
+    // (2r0, 2r0+1) of a chunk; the widening regroups them into token pairs
+    // at head dims 2r0 (accumulator row r0) and 2r0 + 1 (row r0 + 8).
+    __device__ __forceinline__ void accumulate(uint32_t v_smem, int slice, const uint32_t (&bh)[MB][NT][2],
+                                               const uint32_t (&bl)[MB][NT][2]) {
+        const uint32_t addr = lane_addr(v_smem, slice);
 #pragma unroll
         for (int pc = 0; pc < KC / 2; ++pc) {
-            const int chunk = 2 * pc + (mi >> 1);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                const int lrow = base + 16 * mb + rr + 8 * (mi & 1);
                 uint32_t a[4];
-                ldsm_x4_trans(v_smem + lrow * kRowBytes + (swz(chunk, lrow) << 4), a[0], a[1], a[2], a[3]);
+                ldsm_x4_trans((addr ^ (pc << 5)) + mb * 16 * kRowBytes, a[0], a[1], a[2], a[3]);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     // tokens 0..7 (x) and 8..15 (y) of the block, chunk 2pc + half
@@ -448,6 +361,181 @@ struct QuantConsumer {
                 }
             }
         }
+    }
+
+    // Mask x[mb][nt][..]: token r of block mb is inside column e's causal
+    // range when r < valid - 16 mb - shift.
+    __device__ __forceinline__ void mask(float (&x)[4], int nt, int vmb) {
+        const int r0 = (threadIdx.x & 31) >> 2;
+        const int va = vmb - shift[nt][0], vb = vmb - shift[nt][1];
+        if (r0 >= va) x[0] = -INFINITY;
+        if (r0 >= vb) x[1] = -INFINITY;
+        if (r0 + 8 >= va) x[2] = -INFINITY;
+        if (r0 + 8 >= vb) x[3] = -INFINITY;
+    }
+
+    // One tile: `slice` = this warp's slice of kWarpTokens tokens (MB blocks
+    // of 16), `valid` = how many of those tokens are inside the row.
+    __device__ __forceinline__ void tile(uint32_t k_smem, uint32_t v_smem, int slice, int valid, float) {
+        const bool ends = valid - (FD_MAX_GROUP - 1) < kWarpTokens;   // some column's range may end in this slice
+        float s[MB][NT][4];
+        uint32_t bh[MB][NT][2], bl[MB][NT][2];
+        logits(k_smem, slice, s);
+        if constexpr (kBlock)
+            softmax_block(s, ends, valid, bh, bl);
+        else
+            softmax(s, ends, valid, bh, bl);
+        if (valid < kWarpTokens) clear_rows(v_smem, slice, valid);
+        accumulate(v_smem, slice, bh, bl);
+    }
+
+    // Online softmax per column with a lazy reference maximum: m moves
+    // (and the accumulators are rescaled) only when a logit of the tile
+    // exceeds it by more than kLazy; otherwise p = 2^(x - m) directly.
+    // x: the tile's products q . k in, logits out.
+    __device__ __forceinline__ void softmax(float (&x)[MB][NT][4], bool ends, int valid, uint32_t (&bh)[MB][NT][2],
+                                            uint32_t (&bl)[MB][NT][2]) {
+        bool grow = false;
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[mb][nt][e] *= colmul[nt][e & 1];
+                if (ends) mask(x[mb][nt], nt, valid - 16 * mb);
+                const float ta = m[nt][0] + kLazy, tb = m[nt][1] + kLazy;
+                grow |= x[mb][nt][0] > ta || x[mb][nt][2] > ta || x[mb][nt][1] > tb || x[mb][nt][3] > tb;
+            }
+        if (__any_sync(0xffffffffu, grow)) {   // the fallback: a synchronised rescale
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float ma = -INFINITY, mbx = -INFINITY;
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    ma = fmaxf(ma, fmaxf(x[mb][nt][0], x[mb][nt][2]));
+                    mbx = fmaxf(mbx, fmaxf(x[mb][nt][1], x[mb][nt][3]));
+                }
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, sh));
+                    mbx = fmaxf(mbx, __shfl_xor_sync(0xffffffffu, mbx, sh));
+                }
+                const float na = fmaxf(m[nt][0], ma), nb = fmaxf(m[nt][1], mbx);
+                const float ua = na == -INFINITY ? 0.f : na, ub = nb == -INFINITY ? 0.f : nb;
+                const float alpha_a = ex2(m[nt][0] - ua), alpha_b = ex2(m[nt][1] - ub);
+                l[nt][0] *= alpha_a;
+                l[nt][1] *= alpha_b;
+                m[nt][0] = na;
+                m[nt][1] = nb;
+                rescale(nt, alpha_a, alpha_b);
+            }
+        }
+        // P^T fragments per block, x 2^kPScale
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float ta = kPScale - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
+            const float tb = kPScale - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const float p0 = ex2(x[mb][nt][0] + ta), p2 = ex2(x[mb][nt][2] + ta);
+                const float p1 = ex2(x[mb][nt][1] + tb), p3 = ex2(x[mb][nt][3] + tb);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                split_p(p0, p1, p2, p3, bh[mb][nt], bl[mb][nt]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void rescale(int nt, float alpha_a, float alpha_b) {
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+            o[nt][c][0] *= alpha_a;
+            o[nt][c][1] *= alpha_b;
+            o[nt][c][2] *= alpha_a;
+            o[nt][c][3] *= alpha_b;
+        }
+    }
+
+    // The same with one scale per block of tokens. With d = m - mo, the tile
+    // takes  p = 2^(x - m + kPScale)  into the sum and  p f,  f = 2^(log2
+    // v_scale + d),  into P V; both references are right as long as neither p
+    // nor p f passes 2^(kLazy + kPScale) (m starts at -1e30, so a first logit
+    // gives p = inf). s: the tile's products q . k.
+    static constexpr float kNoRef = -1e30f;
+    __device__ __forceinline__ void softmax_block(float (&s)[MB][NT][4], bool ends, int valid,
+                                                  uint32_t (&bh)[MB][NT][2], uint32_t (&bl)[MB][NT][2]) {
+        constexpr float kMost = 32768.f;   // 2^(kLazy + kPScale)
+        static_assert(kLazy + kPScale == 15.f, "kMost");
+        float p[MB][NT][4], f[MB][NT][2];
+        float most = 0.f;
+        auto weights = [&] {
+            most = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float ta = kPScale - m[nt][0], tb = kPScale - m[nt][1];
+                const float da = m[nt][0] - mo[nt][0], db = m[nt][1] - mo[nt][1];
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    const float ca = colmul[nt][0] * ks[mb], cb = colmul[nt][1] * ks[mb];
+                    fma2(s[mb][nt][0], s[mb][nt][1], ca, cb, ta, tb, p[mb][nt][0], p[mb][nt][1]);
+                    fma2(s[mb][nt][2], s[mb][nt][3], ca, cb, ta, tb, p[mb][nt][2], p[mb][nt][3]);
+                    if (ends) mask(p[mb][nt], nt, valid - 16 * mb);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[mb][nt][e] = ex2(p[mb][nt][e]);
+                    f[mb][nt][0] = ex2(lv[mb] + da);
+                    f[mb][nt][1] = ex2(lv[mb] + db);
+                    const float ma = fmaxf(p[mb][nt][0], p[mb][nt][2]), mbx = fmaxf(p[mb][nt][1], p[mb][nt][3]);
+                    most = fmaxf(fmaxf(most, ma), mbx);
+                    most = fmaxf(fmaxf(most, ma * f[mb][nt][0]), mbx * f[mb][nt][1]);
+                }
+            }
+        };
+        weights();
+        if (__any_sync(0xffffffffu, most > kMost)) {   // the fallback: a synchronised rescale of both references
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float xa = kNoRef, xb = kNoRef, ya = kNoRef, yb = kNoRef;
+#pragma unroll
+                for (int mb = 0; mb < MB; ++mb) {
+                    const float ca = colmul[nt][0] * ks[mb], cb = colmul[nt][1] * ks[mb];
+                    float x[4] = {s[mb][nt][0] * ca, s[mb][nt][1] * cb, s[mb][nt][2] * ca, s[mb][nt][3] * cb};
+                    if (ends) mask(x, nt, valid - 16 * mb);
+                    const float ma = fmaxf(x[0], x[2]), mbx = fmaxf(x[1], x[3]);
+                    xa = fmaxf(xa, ma);
+                    xb = fmaxf(xb, mbx);
+                    ya = fmaxf(ya, ma + lv[mb]);
+                    yb = fmaxf(yb, mbx + lv[mb]);
+                }
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, sh));
+                    xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, sh));
+                    ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, sh));
+                    yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, sh));
+                }
+                xa = fmaxf(xa, m[nt][0]);
+                xb = fmaxf(xb, m[nt][1]);
+                ya = fmaxf(ya, mo[nt][0]);
+                yb = fmaxf(yb, mo[nt][1]);
+                l[nt][0] *= ex2(m[nt][0] - xa);
+                l[nt][1] *= ex2(m[nt][1] - xb);
+                rescale(nt, ex2(mo[nt][0] - ya), ex2(mo[nt][1] - yb));
+                m[nt][0] = xa;
+                m[nt][1] = xb;
+                mo[nt][0] = ya;
+                mo[nt][1] = yb;
+            }
+            weights();
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                l[nt][0] += p[mb][nt][0] + p[mb][nt][2];
+                l[nt][1] += p[mb][nt][1] + p[mb][nt][3];
+                split_p(p[mb][nt][0] * f[mb][nt][0], p[mb][nt][1] * f[mb][nt][1], p[mb][nt][2] * f[mb][nt][0],
+                        p[mb][nt][3] * f[mb][nt][1], bh[mb][nt], bl[mb][nt]);
+            }
     }
 
     // This warp's (o, m, l) into a merge buffer slot: o[G][D] with the head
@@ -466,9 +554,11 @@ struct QuantConsumer {
                 for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
             const int ha = nt * 8 + 2 * cc, hb = ha + 1;
             float va = vmul, vb = vmul;
-            if constexpr (kBlock) {   // from y's reference back to x's; no contribution at all: 0
-                va = mo[nt][0] == -INFINITY ? 0.f : ex2(mo[nt][0] - m[nt][0]);
-                vb = mo[nt][1] == -INFINITY ? 0.f : ex2(mo[nt][1] - m[nt][1]);
+            if constexpr (kBlock) {   // from y's reference back to x's, and the merge's "no token" for a column without
+                va = ex2(mo[nt][0] - m[nt][0]);
+                vb = ex2(mo[nt][1] - m[nt][1]);
+                if (m[nt][0] == kNoRef) m[nt][0] = -INFINITY;
+                if (m[nt][1] == kNoRef) m[nt][1] = -INFINITY;
             }
             // dims d0 and d0 + 1 of one head as one 8-byte store; with the padded
             // head stride the 16 lanes of each half warp fill all 32 banks
