@@ -99,6 +99,9 @@ struct QuantConsumer {
     float ks[MB], lv[MB];                   // this tile's key scales and log2 of its value scales
     float ks_next[MB], vs_next[MB];         // the group's next tile's scales, on their way
     int page_next[MB];                      // paged: the pages of the tile after that
+    const float *kp, *vp;                   // the row's (paged: the head's) scales
+    const int32_t *table;                   // paged: the sequence's pages
+    int last;                               // the row's last token
 
     __device__ __forceinline__ void init(const SplitParams &p) {
         const int cc = (threadIdx.x & 31) & 3;
@@ -121,65 +124,72 @@ struct QuantConsumer {
         }
     }
 
-    // Pages of the slice's 16-token blocks from token t0 on; -1 past the row
-    // (t0 < 0: no such tile) and for entries outside the pool.
-    __device__ __forceinline__ void fetch_pages(const SplitParams &p, int b, int t0, int L) {
+    // Pages of the slice's 16-token blocks from token t0 on (past the row: of its last token).
+    __device__ __forceinline__ void fetch_pages(const SplitParams &p, int t0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            const int t = t0 + 16 * mb;
-            page_next[mb] = -1;
-            if (t0 >= 0 && t < L && FD_DCHECK(b < p.B && (t >> p.page_shift) < p.max_pages))
-                page_next[mb] = __ldcg(p.block_table + static_cast<size_t>(b) * p.max_pages + (t >> p.page_shift));
+            const int t = min(t0 + 16 * mb, last);
+            page_next[mb] = FD_DCHECK(t >= 0 && (t >> p.page_shift) < p.max_pages) ? __ldcg(table + (t >> p.page_shift)) : -1;
         }
     }
 
     // Start the loads of the scales of the slice's 16-token blocks from token
-    // t0 on; 0 for blocks past the row. L2 loads: the kernel before this one
-    // on the stream may have written them after this grid began.
-    __device__ __forceinline__ void fetch_scales(const SplitParams &p, const Cursor &c, int t0, int L) {
+    // t0 on. Blocks past the row take its last token's (their weights are 0
+    // whatever the factor); pages outside the pool read as zeros. L2 loads:
+    // the kernel before this one on the stream may have written them after
+    // this grid began.
+    __device__ __forceinline__ void fetch_scales(const SplitParams &p, int t0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            const int t = t0 + 16 * mb;
-            ks_next[mb] = vs_next[mb] = 0.f;
-            if (t0 < 0 || t >= L) continue;
-            size_t at;
+            if (mb > 0 && p.blk_shift > 4) continue;   // a slice of 32 tokens is aligned: one scale
+            const int t = min(t0 + 16 * mb, last);
             if constexpr (kPagedScales) {
                 const int page = page_next[mb];
-                if (page < 0 || page >= p.num_pages) continue;   // reads as a page of zeros
-                at = (static_cast<size_t>(page) * p.Hkv + c.h) * p.blocks +
-                     ((t & ((1 << p.page_shift) - 1)) >> p.blk_shift);
+                ks_next[mb] = vs_next[mb] = 0.f;
+                if (page < 0 || page >= p.num_pages) continue;
+                const size_t at = static_cast<size_t>(page) * p.Hkv * p.blocks +
+                                  ((t & ((1 << p.page_shift) - 1)) >> p.blk_shift);
+                ks_next[mb] = __ldcg(kp + at);
+                vs_next[mb] = __ldcg(vp + at);
             } else {
-                at = (static_cast<size_t>(c.b) * p.Hkv + c.h) * p.blocks + (t >> p.blk_shift);
-                if (!FD_DCHECK((t >> p.blk_shift) < p.blocks)) continue;
+                const int i = t >> p.blk_shift;
+                if (!FD_DCHECK(i >= 0 && i < p.blocks)) continue;
+                ks_next[mb] = __ldcg(kp + i);
+                vs_next[mb] = __ldcg(vp + i);
             }
-            ks_next[mb] = __ldcg(p.k_scale + at);
-            vs_next[mb] = __ldcg(p.v_scale + at);
         }
     }
+
+    static constexpr int kStride = kCW * kTok;   // tokens from one tile of a group to its next
 
     // Segment start: the scales of the group's first tile (t0: first token of
     // this warp's slice in it).
     __device__ __forceinline__ void start_segment(const SplitParams &p, const Cursor &c, int t0, int, int L) {
+        last = L - 1;
+        const size_t row = kPagedScales ? static_cast<size_t>(c.h) : static_cast<size_t>(c.b) * p.Hkv + c.h;
+        kp = p.k_scale + row * p.blocks;
+        vp = p.v_scale + row * p.blocks;
         if constexpr (kPagedScales) {
-            fetch_pages(p, c.b, t0, L);
-            fetch_scales(p, c, t0, L);
-            fetch_pages(p, c.b, t0 + kCW * kTok, L);
+            table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;
+            fetch_pages(p, t0);
+            fetch_scales(p, t0);
+            fetch_pages(p, t0 + kStride);
         } else {
-            fetch_scales(p, c, t0, L);
+            fetch_scales(p, t0);
         }
     }
 
     // Before a tile: its scales have been asked for a tile ago; ask for those
-    // of the group's next one (first token t_next, -1 if the segment ends).
-    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int, int t_next, int L) {
+    // of the group's next one.
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &, int t0, int, int) {
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            ks[mb] = ks_next[mb];
-            lv[mb] = lg2(vs_next[mb]);
+        for (int mb = 0; mb < MB; ++mb) {   // (copied here, not where they are asked for: a copy waits for its load)
+            const bool first = mb > 0 && p.blk_shift > 4;
+            ks[mb] = first ? ks[0] : ks_next[mb];
+            lv[mb] = first ? lv[0] : lg2(vs_next[mb]);
         }
-        fetch_scales(p, c, t_next, L);
-        if constexpr (kPagedScales)
-            fetch_pages(p, c.b, t_next < 0 ? -1 : t_next + kCW * kTok, L);
+        fetch_scales(p, t0 + kStride);
+        if constexpr (kPagedScales) fetch_pages(p, t0 + 2 * kStride);
     }
 
     __device__ __forceinline__ void reset() {
@@ -459,9 +469,9 @@ struct QuantConsumer {
     // The same with one scale per block of tokens. With d = m - mo, the tile
     // takes  p = 2^(x - m + kPScale)  into the sum and  p f,  f = 2^(log2
     // v_scale + d),  into P V; both references are right as long as neither p
-    // nor p f passes 2^(kLazy + kPScale) (m starts at -1e30, so a first logit
+    // nor p f passes 2^(kLazy + kPScale) (m starts at -3e38, so a first logit
     // gives p = inf). s: the tile's products q . k.
-    static constexpr float kNoRef = -1e30f;
+    static constexpr float kNoRef = -3e38f;
     __device__ __forceinline__ void softmax_block(float (&s)[MB][NT][4], bool ends, int valid,
                                                   uint32_t (&bh)[MB][NT][2], uint32_t (&bl)[MB][NT][2]) {
         constexpr float kMost = 32768.f;   // 2^(kLazy + kPScale)
