@@ -50,11 +50,27 @@ struct EvictParams {
     int B, Hkv, Lmax, keep, recent, out_len;
 };
 
-// Unsigned order of totals: NaN first, then -inf .. +inf, -0 as +0.
+// Unsigned order of totals: NaN first (1), then -inf .. +inf, -0 as +0. 0
+// is below them all and stands for "no token" in a batch's last part.
 __device__ __forceinline__ uint32_t order_key(float w) {
-    if (w != w) return 0u;
     const uint32_t u = __float_as_uint(w + 0.f);
-    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    const uint32_t k = static_cast<int32_t>(u) < 0 ? ~u : u | 0x80000000u;
+    return w != w ? 1u : k;
+}
+
+// Sum of the 32 words of histogram row `bin`, which it clears. Lanes of a warp
+// start on different 16-byte columns: no bank conflicts.
+__device__ __forceinline__ uint32_t take_row(uint32_t *hist, int bin) {
+    uint4 *row = reinterpret_cast<uint4 *>(hist + bin * 32);
+    uint32_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int q = (j + bin) & 7;
+        const uint4 v = row[q];
+        row[q] = make_uint4(0, 0, 0, 0);
+        sum += (v.x + v.y) + (v.z + v.w);
+    }
+    return sum;
 }
 
 // kT threads: 256 for slices of up to 4096 tokens (more rows at once on an
@@ -64,18 +80,19 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
     constexpr int kWarps = kT / 32;
     constexpr int kBatch = kT * kKeys;           // tokens of one batch of a slice
     constexpr int kCounts = kKeys * kWarps;
-    __shared__ uint32_t hist[kBins * 32];        // this block's histogram, one column of bins per lane
+    __shared__ __align__(16) uint32_t hist[kBins * 32];   // this block's histogram, one column of bins per lane
     __shared__ uint32_t bins[2][kBins];          // its sums, by turns: the cluster reads one while the next is made
-    __shared__ uint32_t counts[kCounts];        // a batch's (above | equal << 16) by step and warp
+    __shared__ uint32_t counts[kCounts];         // a batch's (above | equal << 16) by step and warp
     __shared__ uint32_t warp_sums[kWarps];
     __shared__ uint32_t found[3];                // digit, keys above it, keys in it
     __shared__ uint32_t slice_sums[2];           // kept-above and equal keys of this block's slice
 
     cg::cluster_group cluster = cg::this_cluster();
     const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
-    grid_dependents_launch();
-    grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependents_launch();
+    for (int i = tid; i < kBins * 32 / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
+    grid_dependency_wait();
     const long long u = blockIdx.x / C;
     const int b = static_cast<int>(u / p.Hkv), h = static_cast<int>(u - static_cast<long long>(b) * p.Hkv);
     const int L = clamp_len(__ldcg(p.seqlens + b), p.Lmax);
@@ -93,64 +110,60 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
 
     // this block's slice [lo, hi) of the candidates
     const long long slice = (static_cast<long long>(M) + C - 1) / C;
-    const int lo = static_cast<int>(min(rank * slice, static_cast<long long>(M)));
-    const int hi = static_cast<int>(min(lo + slice, static_cast<long long>(M)));
+    const long long lo = min(rank * slice, static_cast<long long>(M)), hi = min(lo + slice, static_cast<long long>(M));
     const float *w = p.w + static_cast<size_t>(u) * p.Lmax;
     const bool resident = slice <= kBatch;
     uint32_t key[kKeys];
-    // the batch's keys, thread-striped: token base + i * kT + tid, inside the
-    // slice while i * kT < left(base)
-    auto left = [&](long long base) { return static_cast<int>(min(hi - base, static_cast<long long>(kBatch))) - tid; };
+    // the batch's keys, thread-striped (token base + i * kT + tid)
     auto load = [&](long long base) {
-        const int n_left = left(base);
+        const int n_left = static_cast<int>(min(hi - base, static_cast<long long>(kBatch))) - tid;
         const float *at = w + base + tid;
+        float x[kKeys];
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) key[i] = i * kT < n_left ? __float_as_uint(__ldcg(at + i * kT)) : 0u;
+        for (int i = 0; i < kKeys; ++i) x[i] = i * kT < n_left ? __ldcg(at + i * kT) : 0.f;
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) key[i] = order_key(__uint_as_float(key[i]));
+        for (int i = 0; i < kKeys; ++i) key[i] = i * kT < n_left ? order_key(x[i]) : 0u;
     };
     if (resident) load(lo);
+    __syncthreads();   // hist is clear
 
-    uint32_t prefix = 0, mask = 0, need = static_cast<uint32_t>(k);
+    uint32_t prefix = 0, need = static_cast<uint32_t>(k);
+    int shift = 32;           // the key's bits from `shift` up are settled: they are prefix's
     bool whole_bin = false;   // every key that matches the prefix is kept
-#pragma unroll 1
-    for (int pass = 0; pass < 4 && !whole_bin; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int i = tid; i < kBins * 32 / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+        constexpr int kDigit = 8;
+        if (whole_bin) break;
+        const int down = 24 - kDigit * pass;
         for (long long base = lo; base < hi; base += kBatch) {
             if (!resident) load(base);
-            const int n_left = left(base);
 #pragma unroll
             for (int i = 0; i < kKeys; ++i)
-                if (i * kT < n_left && (key[i] & mask) == prefix)
-                    atomicAdd(&hist[((key[i] >> shift) & 255u) * 32 + lane], 1u);
+                if (pass == 0 || (key[i] >> (down + (pass == 0 ? 0 : kDigit))) == (prefix >> (down + (pass == 0 ? 0 : kDigit))))
+                    atomicAdd(&hist[((key[i] >> down) & 255u) * 32 + lane], 1u);
         }
         __syncthreads();
-        uint32_t *mine = bins[pass & 1];
-#pragma unroll
-        for (int i = 0; i < kBins / kWarps; ++i) {
-            const int bin = warp * (kBins / kWarps) + i;
-            const uint32_t sum = __reduce_add_sync(0xffffffffu, hist[bin * 32 + lane]);
-            if (lane == 0) mine[bin] = sum;
-        }
         // the digit whose bin holds the need-th key of the cluster from the
-        // top: thread i looks at bin 255 - i. The other block's bins of this
-        // pass are whole after the cluster barrier, and written again two
-        // passes on, after the next one.
-        if (C > 1)
-            cluster.sync();
-        else
-            __syncthreads();
+        // top: thread i takes bin 255 - i, which it sums and clears. Another
+        // block's bins of this pass are whole after the cluster barrier, and
+        // written again two passes on, after the next one.
         uint32_t c = 0, incl = 0;
-        if (tid < kBins) {
-            const int bin = kBins - 1 - tid;
-            if (C > 1) {
-#pragma unroll 8
-                for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(mine, r)[bin];
-            } else {
-                c = mine[bin];
+        const int bin = kBins - 1 - tid;
+        if (tid < kBins) c = take_row(hist, bin);
+        if (C > 1) {
+            uint32_t *mine = bins[pass & 1];
+            if (tid < kBins) mine[bin] = c;
+            cluster.sync();
+            if (tid < kBins) {
+                uint32_t others[8];   // all remote reads on their way at once (C <= 8)
+#pragma unroll
+                for (int r = 0; r < 8; ++r) others[r] = r < C ? cluster.map_shared_rank(mine, r)[bin] : 0u;
+                c = 0;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) c += others[r];
             }
+        }
+        if (tid < kBins) {
             incl = c;
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
@@ -162,41 +175,37 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
         __syncthreads();
         if (tid < kBins) {
             uint32_t before = incl - c;
-            for (int i = 0; i < warp; ++i) before += warp_sums[i];
+#pragma unroll
+            for (int i = 0; i < kBins / 32; ++i) before += i < warp ? warp_sums[i] : 0u;
             if (before < need && before + c >= need) {
-                found[0] = static_cast<uint32_t>(kBins - 1 - tid);
+                found[0] = static_cast<uint32_t>(bin);
                 found[1] = before;
                 found[2] = c;
             }
         }
         __syncthreads();
-        prefix |= found[0] << shift;
-        mask |= 255u << shift;
+        prefix |= found[0] << down;
+        shift = down;
         need -= found[1];
         whole_bin = found[2] == need;
         // (found is written again only after the next pass's barriers)
     }
-    // kept: (key & mask) > prefix, and the first `need` with (key & mask) == prefix
+    // kept: keys above `top`, and the first `need` of those from `prefix` to `top`
+    const uint32_t top = prefix | ((1u << shift) - 1u);
 
-    // The batch's tokens above the threshold and equal to it, as bits of two
-    // masks a thread; their counts by step and warp become exclusive sums in
-    // token order (packed above | equal << 16: at most 16384 of each kind).
+    // The batch's counts of both kinds by step and warp become exclusive sums
+    // in token order (packed above | equal << 16: at most 16384 of each kind).
     // Returns the batch's total.
-    uint32_t gt_bits = 0, eq_bits = 0;
-    auto rank_batch = [&](long long base) -> uint32_t {
-        const int n_left = left(base);
-        gt_bits = eq_bits = 0;
-        __syncthreads();   // the last batch's sums have been read
+    auto rank_batch = [&]() -> uint32_t {
+        uint32_t n_mine = 0;   // lane i: step i's counts
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const uint32_t kk = key[i] & mask;
-            const bool in = i * kT < n_left, g = in && kk > prefix, e = in && kk == prefix;
-            gt_bits |= g ? 1u << i : 0u;
-            eq_bits |= e ? 1u << i : 0u;
-            const uint32_t n = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, g))) |
-                               (static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, e))) << 16);
-            if (lane == 0) counts[i * kWarps + warp] = n;
+            const uint32_t ng = __popc(__ballot_sync(0xffffffffu, key[i] > top));
+            const uint32_t ne = __popc(__ballot_sync(0xffffffffu, key[i] >= prefix)) - ng;
+            if (lane == i) n_mine = ng | (ne << 16);
         }
+        __syncthreads();   // the last batch's sums have been read
+        if (lane < kKeys) counts[lane * kWarps + warp] = n_mine;
         __syncthreads();
         uint32_t c = 0, incl = 0;
         if (tid < kCounts) {
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
         __syncthreads();
         return total;
     };
-    static_assert(kCounts <= kT && kCounts % 32 == 0, "one scan of the counts");
+    static_assert(kKeys <= 32 && kCounts <= kT && kCounts % 32 == 0, "one scan of the counts");
     static_assert(kBatch < 65536, "packed counts");
 
     uint32_t gt_before = 0, eq_before = 0, total = 0;
@@ -229,7 +238,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
         uint32_t gt = 0, eq = 0;
         for (long long base = lo; base < hi; base += kBatch) {
             if (!resident) load(base);
-            total = rank_batch(base);
+            total = rank_batch();
             gt += total & 0xffffu;
             eq += total >> 16;
         }
@@ -246,16 +255,17 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
     const unsigned lower = (1u << lane) - 1u;
     for (long long base = lo; base < hi; base += kBatch) {
         if (!resident) load(base);
-        if (C == 1 || !resident) total = rank_batch(base);   // (one batch: still there)
+        if (C == 1 || !resident) total = rank_batch();   // (one batch: still there)
+        const int t_mine = static_cast<int>(base) + tid;
 #pragma unroll
         for (int i = 0; i < kKeys; ++i) {
-            const bool g = (gt_bits >> i) & 1u, e = (eq_bits >> i) & 1u;
-            const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+            const bool g = key[i] > top, ge = key[i] >= prefix;
+            const unsigned bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, ge) & ~bg;
             if ((bg | be) == 0) continue;
             const uint32_t before = counts[i * kWarps + warp];
             const uint32_t gb = gt_before + (before & 0xffffu) + __popc(bg & lower);
             const uint32_t eb = eq_before + (before >> 16) + __popc(be & lower);
-            if (g || (e && eb < need)) kept[gb + min(eb, need)] = static_cast<int>(base) + i * kT + tid;
+            if (g || (ge && eb < need)) kept[gb + min(eb, need)] = t_mine + i * kT;
         }
         gt_before += total & 0xffffu;
         eq_before += total >> 16;
