@@ -14,11 +14,10 @@
 //
 // Select kernel: a cluster of 1 to 8 blocks per row, each with a contiguous
 // slice of its tokens; a pass exchanges 256 bins over distributed shared
-// memory. Totals crowd into few digits (a few binades, many zeros), so each
-// lane has its own column of bins: a warp's 32 additions never meet (one
-// shared column per block measured 75 us on a 131072-token row, all of it
-// additions to the same few words). Up to 16 keys a thread stay in registers
-// over all passes; longer slices read their totals again from L2.
+// memory. Totals crowd into few digits (a few binades, many zeros), so a
+// histogram has 8 columns that lanes take by turns: at most 4 additions of a
+// warp meet. Up to 16 keys a thread stay in registers over all passes; longer
+// slices read their totals again from L2.
 // Gather kernel: 16-byte vectors, 64 kept tokens a block, all of a thread's
 // loads in flight before its first store.
 //
@@ -36,6 +35,7 @@ namespace cg = cooperative_groups;
 constexpr int kKeys = 16;                                   // keys a thread of the select kernel holds
 constexpr int kShortSlice = 256 * kKeys;                    // slices that 256 threads hold
 constexpr int kBins = 256;
+constexpr int kCols = 8;                                    // histogram columns: lanes 8 apart share one
 constexpr int kGatherThreads = 256;
 constexpr int kGatherTokens = 64;
 
@@ -58,16 +58,14 @@ __device__ __forceinline__ uint32_t order_key(float w) {
     return w != w ? 1u : k;
 }
 
-// Sum of the 32 words of histogram row `bin`, which it clears. Lanes of a warp
-// start on different 16-byte columns: no bank conflicts.
+// Sum of the words of histogram row `bin`, which it clears.
 __device__ __forceinline__ uint32_t take_row(uint32_t *hist, int bin) {
-    uint4 *row = reinterpret_cast<uint4 *>(hist + bin * 32);
+    uint4 *row = reinterpret_cast<uint4 *>(hist + bin * kCols);
     uint32_t sum = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int q = (j + bin) & 7;
-        const uint4 v = row[q];
-        row[q] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kCols / 4; ++j) {
+        const uint4 v = row[j];
+        row[j] = make_uint4(0, 0, 0, 0);
         sum += (v.x + v.y) + (v.z + v.w);
     }
     return sum;
@@ -80,7 +78,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
     constexpr int kWarps = kT / 32;
     constexpr int kBatch = kT * kKeys;           // tokens of one batch of a slice
     constexpr int kCounts = kKeys * kWarps;
-    __shared__ __align__(16) uint32_t hist[kBins * 32];   // this block's histogram, one column of bins per lane
+    __shared__ __align__(16) uint32_t hist[kBins * kCols];   // this block's histogram
     __shared__ uint32_t bins[2][kBins];          // its sums, by turns: the cluster reads one while the next is made
     __shared__ uint32_t counts[kCounts];         // a batch's (above | equal << 16) by step and warp
     __shared__ uint32_t warp_sums[kWarps];
@@ -91,7 +89,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
     const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependents_launch();
-    for (int i = tid; i < kBins * 32 / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < kBins * kCols / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
     grid_dependency_wait();
     const long long u = blockIdx.x / C;
     const int b = static_cast<int>(u / p.Hkv), h = static_cast<int>(u - static_cast<long long>(b) * p.Hkv);
@@ -140,7 +138,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
 #pragma unroll
             for (int i = 0; i < kKeys; ++i)
                 if (pass == 0 || (key[i] >> (down + (pass == 0 ? 0 : kDigit))) == (prefix >> (down + (pass == 0 ? 0 : kDigit))))
-                    atomicAdd(&hist[((key[i] >> down) & 255u) * 32 + lane], 1u);
+                    atomicAdd(&hist[((key[i] >> down) & 255u) * kCols + (lane & (kCols - 1))], 1u);
         }
         __syncthreads();
         // the digit whose bin holds the need-th key of the cluster from the
