@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
             gt_before += cluster.map_shared_rank(slice_sums, r)[0];
             eq_before += cluster.map_shared_rank(slice_sums, r)[1];
         }
+        cluster.barrier_arrive();   // this thread reads no other block's memory from here on
     }
     const unsigned lower = (1u << lane) - 1u;
     for (long long base = lo; base < hi; base += kBatch) {
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
         gt_before += total & 0xffffu;
         eq_before += total >> 16;
     }
-    if (C > 1) cluster.sync();   // no block leaves while another reads its shared memory
+    if (C > 1) cluster.barrier_wait();   // no block leaves while another reads its shared memory
 }
 
 template <int D>
@@ -374,7 +375,8 @@ int fd_evict(int B, int Hkv, int D, int max_len, int keep, int recent, int out_l
     p.out_len = out_len;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // blocks per row: more while a slice is longer than 4096 tokens and the
-    // rows leave SMs idle
+    // rows leave SMs idle; 8 at most (clusters of 16 of these blocks fit the
+    // device 7 at a time, one fewer than the rows of a long single sequence)
     int C = 1;
     while (C < 8 && max_len / C > fd::kShortSlice && static_cast<long long>(rows) * C * 2 <= sms) C *= 2;
     const dim3 blocks(static_cast<unsigned>(rows * C));
