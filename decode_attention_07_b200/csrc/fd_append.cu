@@ -110,6 +110,37 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&v)[4]) {
     v[3] = f16hi_to_f32(hi);
 }
 
+// Eight bf16 values at `at` to codes, for any scale.
+template <bool kE4M3>
+__device__ __noinline__ uint2 encode_exactly(const uint16_t *at, float s) {
+    uint32_t w[2];
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t w0 = reinterpret_cast<const uint32_t *>(at)[2 * e];
+        const uint32_t w1 = reinterpret_cast<const uint32_t *>(at)[2 * e + 1];
+        float v[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0), bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
+        for (int k = 0; k < 4; ++k) v[k] = s > 0.f ? to_odd(static_cast<double>(v[k]) / static_cast<double>(s)) : 0.f;
+        w[e] = encode4<kE4M3>(v[0], v[1], v[2], v[3]);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// Eight codes at `at` from scale s_old to the larger s.
+template <bool kE4M3>
+__device__ __noinline__ void recode(uint8_t *at, float s_old, float s) {
+    const uint2 old = __ldcg(reinterpret_cast<const uint2 *>(at));
+    uint32_t w[2] = {old.x, old.y};
+    for (int e = 0; e < 2; ++e) {
+        float v[4];
+        decode4<kE4M3>(w[e], v);
+        for (int k = 0; k < 4; ++k) {
+            v[k] = to_odd(static_cast<double>(v[k]) * s_old / static_cast<double>(s));
+            if (!kE4M3) v[k] = fminf(fmaxf(v[k], -127.f), 127.f);   // the code -128 is not written
+        }
+        w[e] = encode4<kE4M3>(v[0], v[1], v[2], v[3]);
+    }
+    *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+}
+
 // Threads per (block of tokens, head): 8 chunks of 16 bytes each.
 template <int D, int T>
 __host__ __device__ constexpr int append_group() {
@@ -140,6 +171,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fd_append_kernel(const Appe
             const long long t0l = (static_cast<long long>(lo / T) + j) * T;
             if (t0l >= hi || lo >= hi) break;
             const int t0 = static_cast<int>(t0l);
+            // the block's new tokens, in registers (asked for before anything
+            // else is waited for), and their largest magnitude
+            uint4 x[NI];
+            const uint16_t *src = p.src[kv] + b * p.stride_b + h * p.stride_h + col;
+            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+            const uint16_t *at = src + (t0 + row0 - start) * p.stride_t;
+            const long long step = kRows * p.stride_t;
+            const int first = lo - t0 - row0, past = hi - t0 - row0;   // new: i * kRows in [first, past)
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (i * kRows >= first && i * kRows < past) x[i] = __ldcs(reinterpret_cast<const uint4 *>(at));
+                at += step;
+            }
             // where the block's codes and scale are
             uint8_t *codes = p.codes[kv];
             size_t scale_at, row_stride = D;
@@ -162,17 +207,6 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fd_append_kernel(const Appe
             const bool has_old = t0 < lo;
             const float s_old = has_old ? __ldcg(p.scale[kv] + scale_at) : 0.f;
 
-            // the block's new tokens, in registers; their largest magnitude
-            uint4 x[NI];
-            const uint16_t *src = p.src[kv] + b * p.stride_b + h * p.stride_h + col;
-            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int t = t0 + row0 + i * kRows;
-                x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (t >= lo && t < hi)
-                    x[i] = __ldcs(reinterpret_cast<const uint4 *>(src + (t - start) * p.stride_t));
-            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -196,53 +230,28 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fd_append_kernel(const Appe
             if (tid == 0 && !(has_old && s == s_old)) p.scale[kv][scale_at] = s;
             if (fast_scale(s)) {
                 const float rs = __frcp_rn(s);
+                uint8_t *to = codes + row0 * row_stride + col;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    const int r = row0 + i * kRows, t = t0 + r;
-                    if (t < lo || t >= hi) continue;
                     const uint2 c = make_uint2(
                         encode4<kE4M3>(quotient(bf16lo_to_f32(x[i].x), s, rs), quotient(bf16hi_to_f32(x[i].x), s, rs),
                                        quotient(bf16lo_to_f32(x[i].y), s, rs), quotient(bf16hi_to_f32(x[i].y), s, rs)),
                         encode4<kE4M3>(quotient(bf16lo_to_f32(x[i].z), s, rs), quotient(bf16hi_to_f32(x[i].z), s, rs),
                                        quotient(bf16lo_to_f32(x[i].w), s, rs), quotient(bf16hi_to_f32(x[i].w), s, rs)));
-                    *reinterpret_cast<uint2 *>(codes + r * row_stride + col) = c;
+                    if (i * kRows >= first && i * kRows < past) *reinterpret_cast<uint2 *>(to) = c;
+                    to += kRows * row_stride;
                 }
             } else {   // any other scale: 64-bit quotients, the tokens read again
 #pragma unroll 1
-                for (int r = row0; r < T; r += kRows) {
-                    const int t = t0 + r;
-                    if (t < lo || t >= hi) continue;
-                    const uint32_t *at = reinterpret_cast<const uint32_t *>(src + (t - start) * p.stride_t);
-                    uint32_t c[2];
-#pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t w0 = at[2 * e], w1 = at[2 * e + 1];
-                        float v[4] = {bf16lo_to_f32(w0), bf16hi_to_f32(w0), bf16lo_to_f32(w1), bf16hi_to_f32(w1)};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = s > 0.f ? to_odd(static_cast<double>(v[k]) / static_cast<double>(s)) : 0.f;
-                        c[e] = encode4<kE4M3>(v[0], v[1], v[2], v[3]);
-                    }
-                    *reinterpret_cast<uint2 *>(codes + r * row_stride + col) = make_uint2(c[0], c[1]);
-                }
+                for (int r = row0; r < T; r += kRows)
+                    if (t0 + r >= lo && t0 + r < hi)
+                        *reinterpret_cast<uint2 *>(codes + r * row_stride + col) =
+                            encode_exactly<kE4M3>(src + (t0 + r - start) * p.stride_t, s);
             }
             if (has_old && s > s_old) {   // the scale grew: the older codes follow (rare: about log T times a block)
-                for (int r = row0; t0 + r < lo; r += kRows) {
-                    uint2 *at = reinterpret_cast<uint2 *>(codes + r * row_stride + col);
-                    const uint2 c = __ldcg(at);
-                    uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float v[4];
-                        decode4<kE4M3>(w[e], v);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[k] = to_odd(static_cast<double>(v[k]) * s_old / static_cast<double>(s));
-                            if (!kE4M3) v[k] = fminf(fmaxf(v[k], -127.f), 127.f);   // the code -128 is not written
-                        }
-                        w[e] = encode4<kE4M3>(v[0], v[1], v[2], v[3]);
-                    }
-                    *at = make_uint2(w[0], w[1]);
-                }
+#pragma unroll 1
+                for (int r = row0; t0 + r < lo; r += kRows)
+                    recode<kE4M3>(codes + r * row_stride + col, s_old, s);
             }
         }
     }
