@@ -673,7 +673,7 @@ def prepare_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, b
     if Bq != B or Dq != D:
         raise ValueError("q and the cache disagree on B or D")
     _block_outputs(q, out, lse)
-    _seqlens(seqlens, B)
+    _tensor(seqlens, "seqlens", (B,), torch.int32)
     wp, wb = _ws(workspace)
     tensors = (q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, workspace)
     S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
@@ -718,7 +718,7 @@ def prepare_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_t
     if Dq != D or block_table.shape[0] != B:
         raise ValueError("q, pages and block_table disagree on B or D")
     _block_outputs(q, out, lse)
-    _seqlens(seqlens, B)
+    _tensor(seqlens, "seqlens", (B,), torch.int32)
     wp, wb = _ws(workspace)
     tensors = (q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
     S = _planned(q.device.index, B, Hq, Hkv, D, max_pages * page_size, num_splits)
@@ -772,9 +772,7 @@ def _new_tokens(k_new, v_new, B, Hkv, D):
 
 
 def _append_lens(new_lens, seqlens, B):
-    _seqlens(seqlens, B)
-    if not seqlens.is_contiguous():
-        raise ValueError("seqlens must be contiguous")
+    _tensor(seqlens, "seqlens", (B,), torch.int32)
     if new_lens is None:
         return None
     _tensor(new_lens, "new_lens", (B,), torch.int32)
@@ -854,7 +852,7 @@ def prepare_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weight
     B, q_len, Hq, D = _query(q)
     _, _, Hkv, _, Lmax = _shapes(q.view(B, q_len * Hq, D), k_cache, v_cache)
     _block_outputs(q, out, lse)
-    _seqlens(seqlens, B)
+    _tensor(seqlens, "seqlens", (B,), torch.int32)
     for t, name in ((weights_in, "weights_in"), (weights_out, "weights_out")):
         if t is not None or name == "weights_out":
             _tensor(t, name, (B, Hkv, Lmax), torch.float32)

@@ -124,11 +124,14 @@ struct QuantConsumer {
         }
     }
 
+    // A token of the row (unsigned: a tile or two past a row of nearly 2^31 tokens).
+    __device__ __forceinline__ int clip(uint32_t t) const { return static_cast<int>(min(t, static_cast<uint32_t>(last))); }
+
     // Pages of the slice's 16-token blocks from token t0 on (past the row: of its last token).
-    __device__ __forceinline__ void fetch_pages(const SplitParams &p, int t0) {
+    __device__ __forceinline__ void fetch_pages(const SplitParams &p, uint32_t t0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
-            const int t = min(t0 + 16 * mb, last);
+            const int t = clip(t0 + 16 * mb);
             page_next[mb] = FD_DCHECK(t >= 0 && (t >> p.page_shift) < p.max_pages) ? __ldcg(table + (t >> p.page_shift)) : -1;
         }
     }
@@ -138,11 +141,11 @@ struct QuantConsumer {
     // whatever the factor); pages outside the pool read as zeros. L2 loads:
     // the kernel before this one on the stream may have written them after
     // this grid began.
-    __device__ __forceinline__ void fetch_scales(const SplitParams &p, int t0) {
+    __device__ __forceinline__ void fetch_scales(const SplitParams &p, uint32_t t0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
             if (mb > 0 && p.blk_shift > 4) continue;   // a slice of 32 tokens is aligned: one scale
-            const int t = min(t0 + 16 * mb, last);
+            const int t = clip(t0 + 16 * mb);
             if constexpr (kPagedScales) {
                 const int page = page_next[mb];
                 ks_next[mb] = vs_next[mb] = 0.f;

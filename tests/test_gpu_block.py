@@ -181,13 +181,14 @@ def test_one_scale_everywhere_equals_the_per_head_form(kv):
 
 # ------------------------------------------------------------------- pages --
 
-def to_pages(codes, scales, seqlens, ps, T, layout, seed, kv):
-    """Scatter [B,Hkv,L,D] codes and [B,Hkv,nblk] scales into shuffled pages."""
+def to_pages(codes, scales, seqlens, ps, T, layout, seed, kv, inorder=False):
+    """Scatter [B,Hkv,L,D] codes and [B,Hkv,nblk] scales into shuffled pages
+    (inorder: a sequence's pages follow one another in the pool)."""
     B, Hkv, L, D = codes[0].shape
     per = (-(-L // ps) + 3) // 4 * 4
     need = [-(-min(max(n, 0), L) // ps) for n in seqlens]
     pages = sum(need) + 3
-    order = np.random.RandomState(seed).permutation(pages)
+    order = np.arange(pages) if inorder else np.random.RandomState(seed).permutation(pages)
     table = np.full((B, per), 10 ** 6, np.int32)
     shape = (pages, Hkv, ps, D) if layout == "HND" else (pages, ps, Hkv, D)
     pools = [torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda") for _ in codes]
@@ -230,6 +231,43 @@ def test_pages_equal_contiguous(kv, ps, T, layout, g, D, q_len):
         torch.cuda.synchronize()
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), f"S={S}"
         ref.close(a[0], a[1], r, v, D, P_EPS, f"{kv} pages of {ps}, S={S}")
+
+
+@pytest.mark.parametrize("ps,T,layout,D", [(16, 16, "HND", 128), (32, 32, "NHD", 64), (64, 16, "NHD", 128)])
+def test_pages_in_pool_order(ps, T, layout, D):
+    """Small pages that follow one another in the pool come with one copy per tile."""
+    kv, seqlens = "int8", [900, 77, 512]
+    k8, v8, ks, vs = make(3, 2, 900, D, T, kv, seqlens, 20)
+    q = query(3, 1, 8, D, 21)
+    lens = torch.tensor(seqlens, dtype=torch.int32, device="cuda")
+    (kp, vp), (ksp, vsp), table = to_pages([k8, v8], [ks, vs], seqlens, ps, T, layout, 22, kv, inorder=True)
+    a = fd.decode_quant_block_paged(q, kp, vp, ksp, vsp, kv, T, table, lens, 0.1, layout, num_splits=11)
+    b = fd.decode_quant_block(q, k8, v8, ks, vs, kv, T, lens, 0.1, num_splits=11)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_calls_at_once():
+    """Two streams, two workspaces, overlapping on the device."""
+    calls = []
+    for i in range(2):
+        seqlens = [4000, 17, 3999, 2500]
+        k8, v8, ks, vs = make(4, 2, 4000, 128, 64, "e4m3", seqlens, 30 + i)
+        q = query(4, 1, 8, 128, 40 + i)
+        lens = torch.tensor(seqlens, dtype=torch.int32, device="cuda")
+        want = fd.decode_quant_block(q, k8, v8, ks, vs, "e4m3", 64, lens, 0.1, num_splits=37)
+        ws = torch.zeros(fd.quant_workspace_bytes(q, k8, 37), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:-1], device="cuda")
+        side = torch.cuda.Stream()
+        calls.append((fd.prepare_decode_quant_block(q, k8, v8, ks, vs, "e4m3", 64, lens, 0.1, out, lse, ws, 37,
+                                                    stream=side), out, lse, want))
+    torch.cuda.synchronize()
+    for rep in range(20):
+        for call, *_ in calls:
+            call()
+    torch.cuda.synchronize()
+    for _, out, lse, want in calls:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
 def test_a_bad_page_reads_as_zeros():

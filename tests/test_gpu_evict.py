@@ -108,6 +108,7 @@ def test_ties_and_special_totals(kind, L):
 def test_short_empty_and_clamped_rows():
     w = totals(6, 2, 300, 7)
     check(w, [0, 100, 101, 300, 900, -4], 100, 20, out_len=150)
+    check(w, [0, 100, 101, 300, 900, -4], 400, 20, out_len=401)      # a budget beyond the cache
 
 
 def test_offsets_past_32_bits():
