@@ -90,9 +90,9 @@ __global__ void __launch_bounds__(kT) fd_select_kernel(const EvictParams p) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependents_launch();
     for (int i = tid; i < kBins * kCols / 4; i += kT) reinterpret_cast<uint4 *>(hist)[i] = make_uint4(0, 0, 0, 0);
-    grid_dependency_wait();
     const long long u = blockIdx.x / C;
     const int b = static_cast<int>(u / p.Hkv), h = static_cast<int>(u - static_cast<long long>(b) * p.Hkv);
+    grid_dependency_wait();
     const int L = clamp_len(__ldcg(p.seqlens + b), p.Lmax);
     int32_t *kept = p.kept + static_cast<size_t>(u) * p.keep;
     const int n = min(L, p.keep);
@@ -284,25 +284,25 @@ __global__ void __launch_bounds__(kGatherThreads) fd_gather_kernel(const EvictPa
     for (long long item = blockIdx.x; item < total; item += gridDim.x) {
         const long long u = item / chunks;
         const int s0 = static_cast<int>((item - u * chunks) * kGatherTokens);
-        const int b = static_cast<int>(u / p.Hkv);
-        const int n = min(clamp_len(__ldcg(p.seqlens + b), p.Lmax), p.keep);
-        __syncthreads();
-        if (tid < kGatherTokens && s0 + tid < p.out_len) {
+        __syncthreads();   // the last item's positions have been read
+        if (tid < kGatherTokens) {
             const int s = s0 + tid;
-            const int t = s < n ? __ldcg(p.kept + static_cast<size_t>(u) * p.keep + s) : 0;
+            const int t = s < p.keep ? __ldcg(p.kept + static_cast<size_t>(u) * p.keep + s) : -1;
             idx[tid] = t;
-            p.w_out[static_cast<size_t>(u) * p.out_len + s] = s < n ? __ldcg(p.w + static_cast<size_t>(u) * p.Lmax + t) : 0.f;
+            if (s < p.out_len)
+                p.w_out[static_cast<size_t>(u) * p.out_len + s] =
+                    t >= 0 ? __ldcg(p.w + static_cast<size_t>(u) * p.Lmax + t) : 0.f;
         }
         __syncthreads();
-        if (s0 >= n) continue;
+        if (idx[0] < 0) continue;   // kept positions come first
         const uint16_t *k = p.k + static_cast<size_t>(u) * p.Lmax * D + col;
         const uint16_t *v = p.v + static_cast<size_t>(u) * p.Lmax * D + col;
         uint4 x[NI], y[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int r = row0 + i * kRows;
-            if (s0 + r < n) {
-                const size_t at = static_cast<size_t>(idx[r]) * D;
+            const int t = idx[row0 + i * kRows];
+            if (t >= 0) {
+                const size_t at = static_cast<size_t>(t) * D;
                 x[i] = __ldcs(reinterpret_cast<const uint4 *>(k + at));
                 y[i] = __ldcs(reinterpret_cast<const uint4 *>(v + at));
             }
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kGatherThreads) fd_gather_kernel(const EvictPa
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int r = row0 + i * kRows;
-            if (s0 + r < n) {
+            if (idx[r] >= 0) {
                 *reinterpret_cast<uint4 *>(p.k_out + out + static_cast<size_t>(r) * D) = x[i];
                 *reinterpret_cast<uint4 *>(p.v_out + out + static_cast<size_t>(r) * D) = y[i];
             }
