@@ -111,9 +111,7 @@ int take_weights_error(int *word);   // fd_weights.cu
 template <int D, class Consumer, bool kFused, bool kPaged>
 int launch_split_t(const CUtensorMap &tk, const CUtensorMap &tv, const fd::SplitParams &p, cudaStream_t st,
                    const CUtensorMap *rk = nullptr, const CUtensorMap *rv = nullptr) {
-    constexpr int groups = Consumer::kWarps * Consumer::kWarpTokens / fd::kTileTokens;
-    constexpr int smem =
-        fd::SplitConfig<D, Consumer::G, Consumer::kElemBytes, kPaged, Consumer::kWarps, groups>::kSmemBytes;
+    constexpr int smem = fd::SplitConfig<D, Consumer::G, Consumer::kElemBytes, kPaged>::kSmemBytes;
     auto kern = fd::fd_split_kernel<D, Consumer, kFused, kPaged>;
     // the attribute is per function and device; set it once per device
     static std::once_flag once[kMaxDevices];
@@ -135,7 +133,7 @@ int launch_split_t(const CUtensorMap &tk, const CUtensorMap &tv, const fd::Split
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(static_cast<unsigned>(p.P));
-    cfg.blockDim = dim3(fd::split_threads<kPaged, Consumer::kWarps>());
+    cfg.blockDim = dim3(fd::split_threads<kPaged>());
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

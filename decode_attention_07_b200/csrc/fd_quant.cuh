@@ -57,9 +57,12 @@
 //     row's largest contribution, not to its largest scale; a zero scale gives
 //     weight 0.
 //   * Consumers are what bounds it next to memory (two consumer warps per
-//     scheduler issue 0.6 instructions a cycle), so the arithmetic counts:
-//     p = 2^(fma(q.k, c, kPScale - m)) and one factor per (block, column) for
-//     the values; the test for a new reference looks at the p themselves.
+//     scheduler; 12 or 16 consumer warps of 16 tokens each were slower, 60 and
+//     61 us against 54 on 64 heads over 131072 int8 tokens), so the arithmetic
+//     counts: p = 2^(fma(q.k, c, kPScale - m)) and one factor per (block,
+//     column) for the values; the test for a new reference looks at the p
+//     themselves. 32 heads over 16384 E4M3 tokens: 27.2 us (one scale per
+//     head 25.8); 64/8 heads over 131072 int8 tokens: 52.3 us (48.6).
 //   * A warp reads its 16-token blocks' scales (through the block table for
 //     paged caches) one tile of its group ahead, with loads from L2, so their
 //     latency lies behind a tile's arithmetic.
@@ -69,8 +72,7 @@
 
 namespace fd {
 
-template <int D, int NT, bool kE4M3, int kTok = 16, bool kBlock = false, bool kPagedScales = false,
-          int kCW = kConsumerWarps>
+template <int D, int NT, bool kE4M3, int kTok = 16, bool kBlock = false, bool kPagedScales = false>
 struct QuantConsumer {
     static constexpr int G = 8 * NT;        // columns held (padded)
     static constexpr int kElemBytes = 1;
@@ -79,7 +81,6 @@ struct QuantConsumer {
     static constexpr int KACC = MB == 1 ? 2 : 1;      // logit accumulators per block
     static constexpr bool kInterleaved = false;
     static constexpr bool kTileHook = kBlock;
-    static constexpr int kWarps = kCW;
     static constexpr int KC = D / 16;       // 16-byte chunks of a token = k-steps of S = m-tiles of O^T
     static constexpr int kRowBytes = D;
     // The reference max lags the running max by at most kLazy (base 2), so
@@ -163,7 +164,7 @@ struct QuantConsumer {
         }
     }
 
-    static constexpr int kStride = kCW * kTok;   // tokens from one tile of a group to its next
+    static constexpr int kStride = kConsumerWarps * kTok;   // tokens from one tile of a group to its next
 
     // Segment start: the scales of the group's first tile (t0: first token of
     // this warp's slice in it).

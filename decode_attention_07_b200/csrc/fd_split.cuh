@@ -56,15 +56,20 @@ namespace fd {
 // type can declare 32 tokens per warp (four groups of two warps).
 constexpr int kGroups = 2;                        // default: consumer groups alternating tiles
 constexpr int kSliceWarps = 4;                    // default: warps per group (16 tokens each)
-constexpr int kConsumerWarps = kGroups * kSliceWarps;   // default: a consumer type can declare another count
+constexpr int kConsumerWarps = kGroups * kSliceWarps;
+constexpr int kConsumerThreads = kConsumerWarps * 32;
+constexpr int kProducerWarp = kConsumerWarps;     // warp 8
 constexpr int kFinisherWarps = 2;                 // warps 9, 10
 constexpr int kFinisherThreads = kFinisherWarps * 32;
+constexpr int kSplitThreads = kConsumerThreads + 32 + kFinisherThreads;
+constexpr int kWorkerThreads = kConsumerThreads + kFinisherThreads;   // all but the producer
 // Paged caches add a second producer, warp 11, that brings the V boxes while
 // warp 8 brings K and the query heads: a TMA copy costs its issuing thread a
 // fixed time, which dominates the small boxes of small pages, and copies from
 // two warps start in parallel.
-template <bool kPaged, int kWarps = kConsumerWarps>   // kWarps: consumer warps
-constexpr int split_threads() { return (kWarps + 1 + kFinisherWarps + (kPaged ? 1 : 0)) * 32; }
+constexpr int kVProducerWarp = kProducerWarp + 1 + kFinisherWarps;
+template <bool kPaged>
+constexpr int split_threads() { return kSplitThreads + (kPaged ? 32 : 0); }
 constexpr int kPendingMax = 4;                    // rows or chunks a block completes (a run cuts at most 2
                                                   // rows; each completed chunk may complete its row)
 constexpr int kBarFinishers = 1, kBarWorkers = 2; // named barrier ids
@@ -163,8 +168,7 @@ __device__ __forceinline__ size_t out_row(const SplitParams &p, int b, int h, in
 }
 
 // E = bytes per cached element: 2 (bf16) or 1 (8-bit codes).
-// CW = consumer warps, CG = consumer groups taking turns on tiles.
-template <int D, int G, int E = 2, bool kPaged = false, int CW = kConsumerWarps, int CG = kGroups>
+template <int D, int G, int E = 2, bool kPaged = false>
 struct SplitConfig {
     static constexpr int kRowBytes = D * E;                                // one token of one head
     static constexpr int kBoxRowBytes = kRowBytes < 128 ? kRowBytes : 128; // a box row = one swizzle span
@@ -175,24 +179,23 @@ struct SplitConfig {
     static constexpr int kQSlotBytes = (G * D * 2 + 1023) / 1024 * 1024;   // query heads of a row (bf16)
     static constexpr int kStageBytes = 2 * kTileBytes + kQSlotBytes;       // multiple of 1024 (swizzle)
     static constexpr int kWarpFloats = merge_warp_floats<D, G>();          // o, m, l of one warp
-    static constexpr int kMergeFloats = CW * kWarpFloats;      // one merge buffer
+    static constexpr int kMergeFloats = kConsumerWarps * kWarpFloats;      // one merge buffer
     static constexpr int kCtrlBytes = 2048;                                // barriers, start info, queue, weights
     static constexpr int kPageBytes = kPageWindow * 4;                     // block-table window (paged)
     static constexpr int kFixedBytes = 1024 + kCtrlBytes + (kPaged ? 2 : 1) * kPageBytes;   // one window per producer
     // 128 KiB of K/V tiles in flight (measured best for bf16: 4 stages at
     // D = 128), as many as fit next to one merge buffer, in whole pairs
     static constexpr int fit_stages(int s) {
-        return s > kStep && kFixedBytes + s * kStageBytes + kMergeFloats * 4 > kSmemLimit ? fit_stages(s - kStep) : s;
+        return s > 2 && kFixedBytes + s * kStageBytes + kMergeFloats * 4 > kSmemLimit ? fit_stages(s - 2) : s;
     }
-    static constexpr int kStep = CG % 2 == 0 ? 2 : CG;
-    static constexpr int kStages = fit_stages((1024 / kRowBytes + kStep - 1) / kStep * kStep);
+    static constexpr int kStages = fit_stages(1024 / kRowBytes);
     static constexpr int kRingBytes = kStages * kStageBytes;
     static constexpr int kMergeBufs = kFixedBytes + kRingBytes + 2 * kMergeFloats * 4 <= kSmemLimit ? 2 : 1;
     static constexpr int kSmemBytes = kFixedBytes + kRingBytes + kMergeBufs * kMergeFloats * 4;
     // Each consumer group owns whole stages: a stage shared by both groups
     // could be waited on two phases ahead of a tile still in flight, where a
     // parity wait would pass on the older phase.
-    static_assert(kStages % kStep == 0, "stages come in pairs, or in whole rounds of the groups");
+    static_assert(kStages % 2 == 0, "stages come in pairs");
     static_assert(kStageBytes % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
     static_assert(kSmemBytes <= kSmemLimit, "shared memory over the limit");
 };
@@ -459,7 +462,7 @@ __device__ __forceinline__ void take_ticket(const SplitParams &p, StartInfo *inf
 // first one thread per head turns the warps' (m, l) into normalised weights
 // w[head][warp] = 2^(m_w - M) / sum_w' 2^(m_w' - M) l_w' and the log-sum-exp,
 // then every output is sum_w w[head][w] * o_w.
-template <int D, int G, int kConsumerWarps, class Bar>
+template <int D, int G, class Bar>
 __device__ __forceinline__ void merge_warps_and_store(const float *merge, float *weights, const SplitParams &p,
                                                       const Cursor &c, bool whole, size_t slot, int tid,
                                                       int nthreads, Bar bar) {
@@ -528,7 +531,6 @@ struct GroupConsumer {
     static constexpr int kWarpTokens = 16;
     static constexpr bool kInterleaved = kInter;
     static constexpr bool kTileHook = kLogits;
-    static constexpr int kWarps = kConsumerWarps;
 
     float *lg;                          // kLogits: logits of this warp's slice of the tile, [token][lcols]
     int lcols;
@@ -757,7 +759,6 @@ struct HeadConsumer {
     static constexpr int NSUB = kTok / 16;     // 16-token halves
     static_assert(kTok == 16 || kTok == 32, "16 or 32 tokens per warp");
     static constexpr bool kTileHook = kLogits;
-    static constexpr int kWarps = kConsumerWarps;
 
     float *lg;                                 // kLogits: logits of this warp's slice of the tile
     uint4 qw;                                  // q[d0 .. d0+7] of this lane's 16-byte chunk (bf16 pairs)
@@ -924,20 +925,15 @@ struct HeadConsumer {
 
 // ------------------------------------------------------------------ kernel --
 template <int D, class Consumer, bool kFused, bool kPaged = false>
-__global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
+__global__ void __launch_bounds__(split_threads<kPaged>(), 1)
     fd_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_kr, const __grid_constant__ CUtensorMap tm_vr,
                     const SplitParams p) {
     constexpr int G = Consumer::G;
-    constexpr int kConsumerWarps = Consumer::kWarps;
-    constexpr int kConsumerThreads = kConsumerWarps * 32;
-    constexpr int kProducerWarp = kConsumerWarps;         // then the finishers, then the V producer of paged caches
-    constexpr int kVProducerWarp = kProducerWarp + 1 + kFinisherWarps;
-    constexpr int kWorkerThreads = kConsumerThreads + kFinisherThreads;   // all but the producers
+    using Cfg = SplitConfig<D, G, Consumer::kElemBytes, kPaged>;
     constexpr int kTok = Consumer::kWarpTokens;          // tokens per consumer warp and tile
     constexpr int kSlices = kTileTokens / kTok;           // warps per consumer group
     constexpr int kGroupsC = kConsumerWarps / kSlices;    // groups taking turns on tiles
-    using Cfg = SplitConfig<D, G, Consumer::kElemBytes, kPaged, kConsumerWarps, kGroupsC>;
     // Each consumer group owns whole stages: a stage shared by two groups could
     // be waited on two phases ahead of a tile still in flight, where a parity
     // wait would pass on the older phase.
@@ -1237,25 +1233,15 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                     mbar_arrive_expect_tx(&full[stage], 2 * Cfg::kTileBytes + qb);
                     load_tile<Cfg, Consumer::kInterleaved>(kt, vt, &tm_k, &tm_v, &full[stage], y, z, policy);
                 } else {
-                    // the tile's tokens [y, y + 64) span one page (page_size >= 64) or
-                    // 64 / page_size pages; pages past the sequence's end are not loaded
-                    // (their rows are masked), so unused block-table entries never matter
-                    const int psize = 1 << p.page_shift;
-                    const int rows = psize < kTileTokens ? psize : kTileTokens;
+                    // the tile's tokens [y, y + 64) span 64 / page_size pages (larger pages: the
+                    // loop above); pages past the sequence's end are not loaded (their rows are
+                    // masked), so unused block-table entries never matter
+                    const int rows = 1 << p.page_shift;
                     const int lp0 = y >> p.page_shift;
-                    const int npages_seq = (L + psize - 1) >> p.page_shift;
-                    const int nsub = psize >= kTileTokens ? 1 : min(kTileTokens >> p.page_shift, npages_seq - lp0);
-                    const int off = psize >= kTileTokens ? (y & (psize - 1)) : 0;
+                    const int npages_seq = (L + rows - 1) >> p.page_shift;
+                    const int nsub = min(kTileTokens >> p.page_shift, npages_seq - lp0);
                     int page[kTileTokens / 8];
-                    int page1 = 0;   // the one page of a tile when page_size >= 64 (kept in a register)
-                    if (psize >= kTileTokens) {
-                        if (c.b == win_b && lp0 >= win_lo && lp0 < win_hi) {
-                            page1 = win[lp0 - win_lo];   // the common case: inside the window
-                        } else if (!page_of(c.b, lp0, &page1)) {
-                            drain_copies<kStages>(full, seq, wbar, win_pending, win_phase);
-                            return;
-                        }
-                    } else {
+                    {
                         // the tile's pages lp0 .. lp0 + nsub - 1 (lp0 a multiple of 64 / page_size):
                         // one window check for all of them, then vector loads from the window
                         // (the window starts at a multiple of 4 pages and is 16-byte aligned)
@@ -1285,7 +1271,7 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                     // small pages: when the tile's pages are consecutive pages of the pool
                     // (an allocator that hands out pages in order), one box of the run maps
                     // brings them all, with the same bytes at the same places
-                    bool run = psize < kTileTokens && nsub == (kTileTokens >> p.page_shift) && page[0] >= 0 &&
+                    bool run = nsub == (kTileTokens >> p.page_shift) && page[0] >= 0 &&
                                page[0] <= p.num_pages - nsub;
 #pragma unroll
                     for (int j = 1; j < kTileTokens / 8; ++j)
@@ -1297,7 +1283,7 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                         // or {element, half, head, token, page} (token-major pages).
                         const uint32_t page_bytes = static_cast<uint32_t>(rows) * D * 2;
                         mbar_arrive_expect_tx(&full[stage], nsub * page_bytes + qb);
-                        const int cz = p.kv_nhd ? c.h : off, cw = p.kv_nhd ? off : c.h;
+                        const int cz = p.kv_nhd ? c.h : 0, cw = p.kv_nhd ? 0 : c.h;
                         const CUtensorMap *map = v_role ? &tm_v : &tm_k;
                         uint8_t *dst = v_role ? vt : kt;
                         if (run)   // box {64, 2, page_size, 1, nsub} (head-major) or {64, 2, 1, page_size, nsub}
@@ -1329,7 +1315,7 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
 #pragma unroll
                         for (int j = 0; j < kTileTokens / 8; ++j) {   // constant indices: page[] stays in registers
                             if (j >= nsub) break;
-                            const int pgj = psize >= kTileTokens ? page1 : page[j];
+                            const int pgj = page[j];
 #pragma unroll
                             for (int bx = 0; bx < Cfg::kBoxes; ++bx) {
                                 const int dst = bx * Cfg::kBoxBytes + j * rows * Cfg::kBoxRowBytes;
@@ -1339,11 +1325,11 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
                                 // a page outside the pool gets a coordinate outside the tensor (zeros)
                                 const bool inside = pgj >= 0 && pgj < p.num_pages;
                                 if (p.kv_nhd) {
-                                    const int zz = inside ? pgj * (1 << p.page_shift) + off : -kTileTokens;
+                                    const int zz = inside ? pgj * rows : -kTileTokens;
                                     tma_load_3d(dstb + dst, map, &full[stage], x, c.h, zz, policy);
                                 } else {
                                     const int zz = inside ? pgj * p.Hkv + c.h : -1;
-                                    tma_load_3d(dstb + dst, map, &full[stage], x, off, zz, policy);
+                                    tma_load_3d(dstb + dst, map, &full[stage], x, 0, zz, policy);
                                 }
                             }
                         }
@@ -1444,7 +1430,7 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
             const size_t slot = static_cast<size_t>(blockIdx.x) + static_cast<size_t>(u);
             const int buf = static_cast<int>(segctr % kBufs);
             wait_bounded(&mfull[buf], (segctr / kBufs) & 1u, abort);
-            merge_warps_and_store<D, G, kConsumerWarps>(merge + buf * Cfg::kMergeFloats, weights, p, c, whole, slot, ftid,
+            merge_warps_and_store<D, G>(merge + buf * Cfg::kMergeFloats, weights, p, c, whole, slot, ftid,
                                         kFinisherThreads, [] { named_barrier_sync(kBarFinishers, kFinisherThreads); });
             named_barrier_sync(kBarFinishers, kFinisherThreads);   // every finisher is done with the buffer
             if (lane == 0) mbar_arrive(&mempty[buf]);
@@ -1468,7 +1454,7 @@ __global__ void __launch_bounds__(split_threads<kPaged, Consumer::kWarps>(), 1)
         const long long u = static_cast<long long>(last_c.b) * p.Hkv + last_c.h;
         const size_t slot = static_cast<size_t>(blockIdx.x) + static_cast<size_t>(u);
         const int buf = static_cast<int>(info->last_buf);
-        merge_warps_and_store<D, G, kConsumerWarps>(merge + buf * Cfg::kMergeFloats, weights, p, last_c, whole, slot, wtid,
+        merge_warps_and_store<D, G>(merge + buf * Cfg::kMergeFloats, weights, p, last_c, whole, slot, wtid,
                                     kWorkerThreads, workers_sync);
         if (kFused && !whole) {
             workers_sync();   // the stores above, before the ticket
