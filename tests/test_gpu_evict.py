@@ -2,6 +2,9 @@
 equal it exactly. And the operators together: score, evict, hold in 8 bits,
 go on decoding."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -10,6 +13,7 @@ import compress_ref as ref
 import decode_attention_07_b200 as fd
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -158,6 +162,60 @@ def test_in_a_graph_and_refusals():
         fd.fd_evict(k, k, w, lens, 1000, 10, k, torch.empty_like(k), torch.empty_like(w),
                     torch.empty((2, 2, 1000), dtype=torch.int32, device="cuda"), torch.empty_like(lens))
     torch.cuda.synchronize()
+
+
+def test_caches_without_room():
+    """max_len = 0: rows without tokens, nothing written past the outputs."""
+    dev = dict(device="cuda")
+    k = torch.zeros((2, 2, 0, 64), dtype=torch.bfloat16, **dev)
+    w = torch.zeros((2, 2, 0), **dev)
+    lens = torch.tensor([0, 5], dtype=torch.int32, **dev)
+    q = torch.ones((2, 4, 64), dtype=torch.bfloat16, **dev)
+    ko, vo, wo, kept, so = fd.evict(k, k, w, lens, 3, 1)
+    out, lse, total = fd.decode_weights(q, k, k, lens, 0.1)
+    k8, v8, ks, vs = fd.empty_quant_block_cache(2, 2, 0, 64, 16)
+    fd.fd_quant_append(q.view(2, 1, 4, 64)[:, :, :2].contiguous(), q.view(2, 1, 4, 64)[:, :, :2].contiguous(), k8, v8, ks,
+                       vs, "int8", 16, lens)
+    out8, lse8 = fd.decode_quant_block(q, k8, v8, ks, vs, "int8", 16, lens, 0.1)
+    torch.cuda.synchronize()
+    assert so.tolist() == [0, 0] and torch.all(kept == -1) and torch.all(wo == 0) and total.numel() == 0
+    for o, l in ((out, lse), (out8, lse8)):
+        assert torch.all(o == 0) and torch.isneginf(l).all()
+
+
+def test_failed_launches_are_reported():
+    """With the library's host-side injection every entry point returns
+    FD_ERR_LAUNCH, writes nothing and leaves the device status clean."""
+    code = """
+import torch, decode_attention_07_b200 as fd
+dev = dict(device="cuda")
+q = torch.ones((1, 4, 64), dtype=torch.bfloat16, **dev)
+k = torch.ones((1, 2, 100, 64), dtype=torch.bfloat16, **dev)
+lens = torch.tensor([100], dtype=torch.int32, **dev)
+w = torch.full((1, 2, 100), 7.0, **dev)
+k8, v8, ks, vs = fd.empty_quant_block_cache(1, 2, 100, 64, 16)
+outs = [torch.full(s, 7.0, **dev) for s in ((1, 4, 64), (1, 4))]
+ko, vo, wo = torch.full_like(k, 7.0), torch.full_like(k, 7.0), torch.full_like(w, 7.0)
+kept, so = torch.full((1, 2, 10), 7, dtype=torch.int32, **dev), torch.full((1,), 7, dtype=torch.int32, **dev)
+ws = torch.zeros(fd.fd_weights_workspace_bytes(1, 1, 4, 2, 64, 100, 1), dtype=torch.uint8, **dev)
+calls = [lambda: fd.fd_decode_quant_block(q, k8, v8, ks, vs, "int8", 16, lens, 0.1, *outs, None, 1),
+         lambda: fd.fd_quant_append(k.transpose(1, 2), k.transpose(1, 2), k8, v8, ks, vs, "int8", 16, lens),
+         lambda: fd.fd_decode_weights(q, k, k, lens, 0.1, *outs, None, w, ws, 1),
+         lambda: fd.fd_evict(k, k, w, lens, 10, 2, ko, vo, wo, kept, so)]
+for call in calls:
+    try:
+        call()
+    except fd.FdError as e:
+        assert e.code == -9, e
+    else:
+        raise AssertionError("no error")
+torch.cuda.synchronize()
+assert fd.fd_device_status() == 0
+assert all(torch.all(t == 7) for t in (*outs, w, ko, vo, wo, kept, so)) and torch.all(k8 == 0) and torch.all(ks == 0)
+"""
+    env = dict(os.environ, FD_TEST_FAIL_LAUNCH="1")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("kv", ["e4m3", "int8"])
