@@ -273,11 +273,11 @@ FD_API int fd_decode_quant_paged(int B, int q_len, int Hq, int Hkv, int D, int p
  * block that holds a cached token (0 stands for a block of zeros); those of
  * other blocks are never used, whatever they hold. block_tokens: 16, 32, 64
  * or 128. The key scale enters the block's logits and the value scale the
- * exponent of the block's weights, so scales of any spread keep their
- * precision relative to the row's largest contribution (a scale below the
- * smallest normal float counts as 0). Everything else, codes, queries,
- * workspace, errors, as in fd_decode_quant; FD_ERR_SHAPE also for
- * block_tokens. */
+ * block's weights, so the output is good relative to the row's largest
+ * contribution, not to its largest scale, for scales within 2^100 of one
+ * another (a scale below the smallest normal float counts as 0). Everything
+ * else, codes, queries, workspace, errors, as in fd_decode_quant;
+ * FD_ERR_SHAPE also for block_tokens. */
 FD_API int fd_decode_quant_block(int B, int q_len, int Hq, int Hkv, int D, int max_len, int block_tokens, int kv_type,
                                  const uint16_t *q, const uint8_t *k_codes, const uint8_t *v_codes,
                                  const float *k_scale, const float *v_scale, const int32_t *seqlens, float scale,
