@@ -51,11 +51,13 @@
 //     x_t = scale log2(e) k_scale[t / T] (q . decode(k_t)),
 //     out = sum_t 2^(x_t - m) v_scale[t / T] decode(v_t) / sum_t 2^(x_t - m).
 //   * The key scale multiplies the block's logits. The value scale joins the
-//     weight: with y_t = x_t + log2 v_scale[t / T], P V takes 2^(y_t - mo) and
-//     the sum 2^(x_t - m), each with a lazy reference maximum of its own, both
-//     moved by the same rare branch. So P keeps its f16 range relative to the
-//     row's largest contribution, not to its largest scale; a zero scale gives
-//     weight 0.
+//     weight: the sum takes p = 2^(x_t - m) and P V takes p r v_scale[t / T],
+//     with a power of two r per column, so that the scale enters as a product.
+//     r is chosen like m, by the same rare branch, to keep the column's largest
+//     contribution p r v_scale in f16's range: P keeps its bits relative to
+//     the row's largest contribution, not to its largest scale or weight. r is
+//     at most 2^126: a column that has met only zero scales, however heavy,
+//     has a finite r, and zero weights times it are zero.
 //   * Consumers are what bounds it next to memory (two consumer warps per
 //     scheduler; 12 or 16 consumer warps of 16 tokens each were slower, 60 and
 //     61 us against 54 on 64 heads over 131072 int8 tokens), so the arithmetic
@@ -96,8 +98,8 @@ struct QuantConsumer {
     float colmul[NT][2];                    // logit multiplier (base 2) of columns 2c, 2c+1
     float kmul, vmul;                       // scale * log2(e) * k_scale[h], and v_scale[h]
     // kBlock only
-    float mo[NT][2];                        // reference max of y = x + log2 v_scale, columns 2c, 2c+1
-    float ks[MB], lv[MB];                   // this tile's key scales and log2 of its value scales
+    float r[NT][2];                         // the power of two in the outputs' weights p r v_scale, columns 2c, 2c+1
+    float ks[MB], vs[MB];                   // this tile's key and value scales
     float ks_next[MB], vs_next[MB];         // the group's next tile's scales, on their way
     int page_next[MB];                      // paged: the pages of the tile after that
     const float *kp, *vp;                   // the row's (paged: the head's) scales
@@ -138,8 +140,9 @@ struct QuantConsumer {
     }
 
     // Start the loads of the scales of the slice's 16-token blocks from token
-    // t0 on. Blocks past the row take its last token's (their weights are 0
-    // whatever the factor); pages outside the pool read as zeros. L2 loads:
+    // t0 on. Blocks past the row take its last token's (their weights are 0,
+    // and stay 0 times any factor that softmax_block makes of a scale); pages
+    // outside the pool read as zeros. L2 loads:
     // the kernel before this one on the stream may have written them after
     // this grid began.
     __device__ __forceinline__ void fetch_scales(const SplitParams &p, uint32_t t0) {
@@ -190,7 +193,7 @@ struct QuantConsumer {
         for (int mb = 0; mb < MB; ++mb) {   // (copied here, not where they are asked for: a copy waits for its load)
             const bool first = mb > 0 && p.blk_shift > 4;
             ks[mb] = first ? ks[0] : ks_next[mb];
-            lv[mb] = first ? lv[0] : lg2(vs_next[mb]);
+            vs[mb] = first ? vs[0] : vs_next[mb];
         }
         fetch_scales(p, t0 + kStride);
         if constexpr (kPagedScales) fetch_pages(p, t0 + 2 * kStride);
@@ -201,7 +204,7 @@ struct QuantConsumer {
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kBlock ? kNoRef : -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
-            if constexpr (kBlock) mo[nt][0] = mo[nt][1] = kNoRef;
+            if constexpr (kBlock) r[nt][0] = r[nt][1] = 1.f;
 #pragma unroll
             for (int c = 0; c < KC; ++c) o[nt][c][0] = o[nt][c][1] = o[nt][c][2] = o[nt][c][3] = 0.f;
         }
@@ -507,12 +510,27 @@ struct QuantConsumer {
         }
     }
 
-    // The same with one scale per block of tokens. With d = m - mo, the tile
-    // takes  p = 2^(x - m + kPScale)  into the sum and  p f,  f = 2^(log2
-    // v_scale + d),  into P V; both references are right as long as neither p
-    // nor p f passes 2^(kLazy + kPScale) (m starts at -3e38, so a first logit
-    // gives p = inf). s: the tile's products q . k.
+    // The same with one scale per block of tokens: the tile takes
+    // p = 2^(x - m + kPScale) into the sum and p f, f = r v_scale, into P V;
+    // m and r are right as long as neither p nor p f passes
+    // 2^(kLazy + kPScale) (m starts at -3e38, so a first logit gives p = inf).
+    // f may pass float's range where the column has contributed next to
+    // nothing so far: the test takes it as it is (inf times a p above 0 asks
+    // for a new r; inf times 0 is NaN, which fmaxf passes over), P takes it
+    // cut to a finite number, so that weight 0 stays 0. After the fallback
+    // only weights below 2^-126 of the column's largest can meet the cut.
+    // m is a whole number, so that r and the references' differences are
+    // exact. s: the tile's products q . k.
     static constexpr float kNoRef = -3e38f;
+    static constexpr float kMaxLog2R = 126.f;     // below it, an output's contribution is no normal float
+    static constexpr float kMaxF = 8.507059e37f;  // 2^126
+    // 2^e of whole e in [-126, 126], and back.
+    static __device__ __forceinline__ float exp2i(float e) {
+        return __uint_as_float(static_cast<uint32_t>(static_cast<int>(e) + 127) << 23);
+    }
+    static __device__ __forceinline__ float log2i(float x) {
+        return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
+    }
     __device__ __forceinline__ void softmax_block(float (&s)[MB][NT][4], bool ends, int valid,
                                                   uint32_t (&bh)[MB][NT][2], uint32_t (&bl)[MB][NT][2]) {
         constexpr float kMost = 32768.f;   // 2^(kLazy + kPScale)
@@ -524,7 +542,6 @@ struct QuantConsumer {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float ta = kPScale - m[nt][0], tb = kPScale - m[nt][1];
-                const float da = m[nt][0] - mo[nt][0], db = m[nt][1] - mo[nt][1];
 #pragma unroll
                 for (int mb = 0; mb < MB; ++mb) {
                     const float ca = colmul[nt][0] * ks[mb], cb = colmul[nt][1] * ks[mb];
@@ -533,49 +550,51 @@ struct QuantConsumer {
                     if (ends) mask(p[mb][nt], nt, valid - 16 * mb);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) p[mb][nt][e] = ex2(p[mb][nt][e]);
-                    f[mb][nt][0] = ex2(lv[mb] + da);
-                    f[mb][nt][1] = ex2(lv[mb] + db);
+                    const float fa = r[nt][0] * vs[mb], fb = r[nt][1] * vs[mb];
                     const float ma = fmaxf(p[mb][nt][0], p[mb][nt][2]), mbx = fmaxf(p[mb][nt][1], p[mb][nt][3]);
                     most = fmaxf(fmaxf(most, ma), mbx);
-                    most = fmaxf(fmaxf(most, ma * f[mb][nt][0]), mbx * f[mb][nt][1]);
+                    most = fmaxf(fmaxf(most, ma * fa), mbx * fb);
+                    f[mb][nt][0] = fminf(fa, kMaxF);
+                    f[mb][nt][1] = fminf(fb, kMaxF);
                 }
             }
         };
         weights();
-        if (__any_sync(0xffffffffu, most > kMost)) {   // the fallback: a synchronised rescale of both references
+        if (__any_sync(0xffffffffu, most > kMost)) {   // the fallback: a synchronised rescale of sum and outputs
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float xa = kNoRef, xb = kNoRef, ya = kNoRef, yb = kNoRef;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    const float ca = colmul[nt][0] * ks[mb], cb = colmul[nt][1] * ks[mb];
-                    float x[4] = {s[mb][nt][0] * ca, s[mb][nt][1] * cb, s[mb][nt][2] * ca, s[mb][nt][3] * cb};
-                    if (ends) mask(x, nt, valid - 16 * mb);
-                    const float ma = fmaxf(x[0], x[2]), mbx = fmaxf(x[1], x[3]);
-                    xa = fmaxf(xa, ma);
-                    xb = fmaxf(xb, mbx);
-                    ya = fmaxf(ya, ma + lv[mb]);
-                    yb = fmaxf(yb, mbx + lv[mb]);
+                for (int e = 0; e < 2; ++e) {
+                    float xm = kNoRef, ym = kNoRef;   // the column's largest logit, and largest log2 of a contribution
+#pragma unroll
+                    for (int mb = 0; mb < MB; ++mb) {
+                        const float c = colmul[nt][e] * ks[mb];
+                        float z[4] = {s[mb][nt][0] * c, s[mb][nt][1] * c, s[mb][nt][2] * c, s[mb][nt][3] * c};
+                        if (ends) mask(z, nt, valid - 16 * mb);
+                        const float x = fmaxf(z[e], z[e + 2]);
+                        xm = fmaxf(xm, x);
+                        ym = fmaxf(ym, x + lg2(vs[mb]));
+                    }
+#pragma unroll
+                    for (int sh = 4; sh < 32; sh <<= 1) {
+                        xm = fmaxf(xm, __shfl_xor_sync(0xffffffffu, xm, sh));
+                        ym = fmaxf(ym, __shfl_xor_sync(0xffffffffu, ym, sh));
+                    }
+                    xm = fmaxf(m[nt][e], ceilf(xm));
+                    const float dm = m[nt][e] - xm;
+                    // relative to the new m: the largest contribution that r stood for so far, and the tile's
+                    const float was = dm - log2i(r[nt][e]);
+                    const float y = fminf(fmaxf(fmaxf(ceilf(ym - xm), was), -kMaxLog2R), kMaxLog2R);
+                    const float alpha = ex2(was - y);
+                    l[nt][e] *= ex2(dm);
+#pragma unroll
+                    for (int c = 0; c < KC; ++c) {
+                        o[nt][c][e] *= alpha;
+                        o[nt][c][e + 2] *= alpha;
+                    }
+                    m[nt][e] = xm;
+                    r[nt][e] = exp2i(-y);
                 }
-#pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) {
-                    xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, sh));
-                    xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, sh));
-                    ya = fmaxf(ya, __shfl_xor_sync(0xffffffffu, ya, sh));
-                    yb = fmaxf(yb, __shfl_xor_sync(0xffffffffu, yb, sh));
-                }
-                xa = fmaxf(xa, m[nt][0]);
-                xb = fmaxf(xb, m[nt][1]);
-                ya = fmaxf(ya, mo[nt][0]);
-                yb = fmaxf(yb, mo[nt][1]);
-                l[nt][0] *= ex2(m[nt][0] - xa);
-                l[nt][1] *= ex2(m[nt][1] - xb);
-                rescale(nt, ex2(mo[nt][0] - ya), ex2(mo[nt][1] - yb));
-                m[nt][0] = xa;
-                m[nt][1] = xb;
-                mo[nt][0] = ya;
-                mo[nt][1] = yb;
-            }
             weights();
         }
 #pragma unroll
@@ -605,9 +624,9 @@ struct QuantConsumer {
                 for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
             const int ha = nt * 8 + 2 * cc, hb = ha + 1;
             float va = vmul, vb = vmul;
-            if constexpr (kBlock) {   // from y's reference back to x's, and the merge's "no token" for a column without
-                va = ex2(mo[nt][0] - m[nt][0]);
-                vb = ex2(mo[nt][1] - m[nt][1]);
+            if constexpr (kBlock) {   // without r, and the merge's "no token" for a column without
+                va = exp2i(-log2i(r[nt][0]));
+                vb = exp2i(-log2i(r[nt][1]));
                 if (m[nt][0] == kNoRef) m[nt][0] = -INFINITY;
                 if (m[nt][1] == kNoRef) m[nt][1] = -INFINITY;
             }

@@ -272,12 +272,14 @@ FD_API int fd_decode_quant_paged(int B, int q_len, int Hq, int Hkv, int D, int p
  * block_tokens)] float32, device, 4-byte aligned, finite and >= 0 for every
  * block that holds a cached token (0 stands for a block of zeros); those of
  * other blocks are never used, whatever they hold. block_tokens: 16, 32, 64
- * or 128. The key scale enters the block's logits and the value scale the
- * block's weights, so the output is good relative to the row's largest
- * contribution, not to its largest scale, for scales within 2^100 of one
- * another (a scale below the smallest normal float counts as 0). Everything
- * else, codes, queries, workspace, errors, as in fd_decode_quant;
- * FD_ERR_SHAPE also for block_tokens. */
+ * or 128. The key scale enters the block's logits and the value scale, as a
+ * product, the block's weights, so the output is good relative to the row's
+ * largest contribution, whatever its scales and their spread. What leaves
+ * float's range may count as 0: a weight below 2^-126 of the row's largest
+ * (that of a block of zeros included), a contribution to the output or a scale
+ * below 2^-126. Value scales above 2^90 may overflow the sums, and logits are
+ * to stay below 2^26 in size. Everything else, codes, queries, workspace,
+ * errors, as in fd_decode_quant; FD_ERR_SHAPE also for block_tokens. */
 FD_API int fd_decode_quant_block(int B, int q_len, int Hq, int Hkv, int D, int max_len, int block_tokens, int kv_type,
                                  const uint16_t *q, const uint8_t *k_codes, const uint8_t *v_codes,
                                  const float *k_scale, const float *v_scale, const int32_t *seqlens, float scale,
