@@ -2,6 +2,7 @@
 names, taking torch tensors. Argument marshalling only -- every step of the
 computation runs in the library's CUDA kernels. There is no fallback: if the
 library is missing or a call fails, an exception is raised."""
+import contextlib
 import ctypes
 import os
 import warnings
@@ -113,6 +114,31 @@ def _stream(stream, device) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+@contextlib.contextmanager
+def _on_stream(stream, device):
+    """For calls that allocate: `stream` (a Stream, a raw handle, None: the
+    current one) as the current stream, so that what is allocated inside is
+    filled in the call's order and, once dropped, only reused after the call.
+    Yields a function that passes on its arguments, the call's results, which
+    the caller goes on using on the stream that was current outside."""
+    if stream is None:
+        yield lambda *tensors: tensors
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    outer = torch.cuda.current_stream(device)
+
+    def hand_over(*tensors):
+        if outer != stream:
+            for t in tensors:
+                t.record_stream(outer)
+        return tensors
+
+    with torch.cuda.stream(stream):
+        yield hand_over
 
 
 def _shapes(q, k_cache, v_cache):
@@ -234,13 +260,14 @@ def decode_multi(q, k_cache, v_cache, seqlens, scale, num_splits=None, stream=No
     """Allocate out / lse / workspace with torch and run fd_decode_multi."""
     B, q_len, Hq, D = q.shape
     Hkv, Lmax = k_cache.shape[1], k_cache.shape[2]
-    S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
-    nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty((B, q_len, Hq, D), dtype=torch.float32, device=q.device)
-    lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
-    fd_decode_multi(q, k_cache, v_cache, seqlens, scale, out, lse, ws, S, stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
+        nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty((B, q_len, Hq, D), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, q_len, Hq), dtype=torch.float32, device=q.device)
+        fd_decode_multi(q, k_cache, v_cache, seqlens, scale, out, lse, ws, S, stream)
+        return hand_over(out, lse)
 
 
 def _paged_shapes(q, k_pages, v_pages, block_table, layout, pool_dtype=torch.bfloat16):
@@ -339,27 +366,29 @@ def decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tab
                                                                    torch.uint8)
     q_len = 1 if q.dim() == 3 else q.shape[1]
     Lmax = max_pages * page_size
-    S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
-    nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    prepare_decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_table, seqlens, scale, out, lse,
-                               ws, layout, S, stream)()
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
+        nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        prepare_decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_table, seqlens, scale, out,
+                                   lse, ws, layout, S, stream)()
+        return hand_over(out, lse)
 
 
 def decode_paged(q, k_pages, v_pages, block_table, seqlens, scale, layout="HND", num_splits=None, stream=None):
     """Allocate out / lse / workspace with torch and run fd_decode_paged."""
     B, Hq, Hkv, D, page_size, num_pages, max_pages = _paged_shapes(q, k_pages, v_pages, block_table, layout)
     Lmax = max_pages * page_size
-    S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
-    nbytes = fd_workspace_bytes(B, Hq, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    fd_decode_paged(q, k_pages, v_pages, block_table, seqlens, scale, out, lse, ws, layout, S, stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
+        nbytes = fd_workspace_bytes(B, Hq, Hkv, D, Lmax, S)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        fd_decode_paged(q, k_pages, v_pages, block_table, seqlens, scale, out, lse, ws, layout, S, stream)
+        return hand_over(out, lse)
 
 
 def fd_workspace_init(workspace, stream=None):
@@ -505,13 +534,14 @@ def decode_quant(q, k_codes, v_codes, k_scale, v_scale, kv_type, seqlens, scale,
     """Allocate out / lse / workspace with torch and run fd_decode_quant."""
     B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
     Hkv, Lmax = k_codes.shape[1], k_codes.shape[2]
-    S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
-    nbytes = quant_workspace_bytes(q, k_codes, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fd_decode_quant(q, k_codes, v_codes, k_scale, v_scale, kv_type, seqlens, scale, out, lse, ws, S, stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
+        nbytes = quant_workspace_bytes(q, k_codes, S)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        fd_decode_quant(q, k_codes, v_codes, k_scale, v_scale, kv_type, seqlens, scale, out, lse, ws, S, stream)
+        return hand_over(out, lse)
 
 
 def fd_merge_partials(part_out, part_lse, out, lse, stream=None):
@@ -555,13 +585,14 @@ def decode(q, k_cache, v_cache, seqlens, scale, num_splits=None, stream=None):
     """Allocate out / lse / workspace with torch and run fd_decode (or
     fd_decode_splits when num_splits is given). Returns (out, lse)."""
     B, Hq, Hkv, D, Lmax = _shapes(q, k_cache, v_cache)
-    S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
-    nbytes = fd_workspace_bytes(B, Hq, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    fd_decode_splits(q, k_cache, v_cache, seqlens, scale, out, lse, ws, S, stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
+        nbytes = fd_workspace_bytes(B, Hq, Hkv, D, Lmax, S)
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty((B, Hq, D), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        fd_decode_splits(q, k_cache, v_cache, seqlens, scale, out, lse, ws, S, stream)
+        return hand_over(out, lse)
 
 
 # -------------------------------------------------------- cache compression --
@@ -700,12 +731,13 @@ def decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tok
     B, _, Hq, D = _query(q)
     S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
     nbytes = quant_workspace_bytes(q, k_codes, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fd_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse, ws, S,
-                          stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        fd_decode_quant_block(q, k_codes, v_codes, k_scale, v_scale, kv_type, block_tokens, seqlens, scale, out, lse, ws,
+                              S, stream)
+        return hand_over(out, lse)
 
 
 def prepare_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
@@ -748,12 +780,13 @@ def decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, blo
     Lmax = max_pages * page_size
     S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
     nbytes = fd_workspace_bytes(B, Hq * q_len, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    fd_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens, scale,
-                                out, lse, ws, layout, S, stream)
-    return out, lse
+    with _on_stream(stream, q.device) as hand_over:
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        fd_decode_quant_block_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_tokens, block_table, seqlens,
+                                    scale, out, lse, ws, layout, S, stream)
+        return hand_over(out, lse)
 
 
 def _new_tokens(k_new, v_new, B, Hkv, D):
@@ -883,13 +916,14 @@ def decode_weights(q, k_cache, v_cache, seqlens, scale, weights=None, num_splits
     _, _, Hkv, _, Lmax = _shapes(q.view(B, q_len * Hq, D), k_cache, v_cache)
     S = _planned(q.device.index, B, Hq, Hkv, D, Lmax, num_splits)
     nbytes = fd_weights_workspace_bytes(B, q_len, Hq, Hkv, D, Lmax, S)
-    ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    if weights is None:
-        weights = torch.zeros((B, Hkv, Lmax), dtype=torch.float32, device=q.device)
-    fd_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights, weights, ws, S, stream)
-    return out, lse, weights
+    with _on_stream(stream, q.device) as hand_over:
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        if weights is None:
+            weights = torch.zeros((B, Hkv, Lmax), dtype=torch.float32, device=q.device)
+        fd_decode_weights(q, k_cache, v_cache, seqlens, scale, out, lse, weights, weights, ws, S, stream)
+        return hand_over(out, lse, weights)
 
 
 def prepare_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, weights_out, kept, seqlens_out,
@@ -934,10 +968,11 @@ def evict(k_cache, v_cache, weights, seqlens, keep, recent=0, out_len=None, stre
     B, Hkv, _, D = k_cache.shape
     n = keep if out_len is None else int(out_len)
     dev = k_cache.device
-    k_out = torch.zeros((B, Hkv, n, D), dtype=torch.bfloat16, device=dev)
-    v_out = torch.zeros_like(k_out)
-    w_out = torch.empty((B, Hkv, n), dtype=torch.float32, device=dev)
-    kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
-    lens = torch.empty((B,), dtype=torch.int32, device=dev)
-    fd_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, w_out, kept, lens, stream)
-    return k_out, v_out, w_out, kept, lens
+    with _on_stream(stream, dev) as hand_over:
+        k_out = torch.zeros((B, Hkv, n, D), dtype=torch.bfloat16, device=dev)
+        v_out = torch.zeros_like(k_out)
+        w_out = torch.empty((B, Hkv, n), dtype=torch.float32, device=dev)
+        kept = torch.empty((B, Hkv, keep), dtype=torch.int32, device=dev)
+        lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        fd_evict(k_cache, v_cache, weights, seqlens, keep, recent, k_out, v_out, w_out, kept, lens, stream)
+        return hand_over(k_out, v_out, w_out, kept, lens)

@@ -51,12 +51,13 @@ def cp_decode(q, k_shard, v_shard, seqlens, lo, scale, group=None, num_splits=No
     """Decode attention of q over a cache sharded across `group`: this rank
     holds positions [lo, lo + k_shard.shape[2]). Returns the merged (out,
     lse), the same on every rank."""
-    part_o, part_l = _lib.decode(q, k_shard, v_shard, local_seqlens(seqlens, lo), scale, num_splits, stream)
-    if group is None and not (torch.distributed.is_available() and torch.distributed.is_initialized()):
-        all_o, all_l = part_o[None], part_l[None]
-    else:
-        all_o, all_l = gather_partials(part_o, part_l, group)
-    out = torch.empty_like(part_o)
-    lse = torch.empty_like(part_l)
-    _lib.fd_merge_partials(all_o, all_l, out, lse, stream)
-    return out, lse
+    with _lib._on_stream(stream, q.device) as hand_over:
+        part_o, part_l = _lib.decode(q, k_shard, v_shard, local_seqlens(seqlens, lo), scale, num_splits)
+        if group is None and not (torch.distributed.is_available() and torch.distributed.is_initialized()):
+            all_o, all_l = part_o[None], part_l[None]
+        else:
+            all_o, all_l = gather_partials(part_o, part_l, group)
+        out = torch.empty_like(part_o)
+        lse = torch.empty_like(part_l)
+        _lib.fd_merge_partials(all_o, all_l, out, lse)
+        return hand_over(out, lse)
