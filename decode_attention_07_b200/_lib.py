@@ -175,6 +175,36 @@ def _ws(workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+def _one_device(*tensors):
+    """Index of the device that holds all of `tensors` (None entries aside)."""
+    devices = {t.device.index for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("all tensors must be on one device")
+    return devices.pop()
+
+
+def _prepared(what, tensors, args):
+    """A no-argument callable that runs entry point `what` with `args`, with
+    the device of `tensors` as the current one. It holds the tensors (None
+    entries aside): their memory stays theirs as long as it lives."""
+    device = _one_device(*tensors)
+    fn = getattr(lib(), what)
+    # converted once here, not on every call
+    args = tuple(t(a) if a is not None else a for t, a in zip(fn.argtypes, args))
+
+    def call():
+        if torch.cuda.current_device() == device:
+            rc = fn(*args)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args)
+        if rc != 0:
+            raise FdError(rc, what)
+
+    call.tensors = tensors
+    return call
+
+
 # ---------------------------------------------------------------- the ABI --
 
 def fd_plan(B: int, Hq: int, Hkv: int, D: int, max_len: int) -> int:
@@ -312,17 +342,10 @@ def prepare_decode_paged(q, k_pages, v_pages, block_table, seqlens, scale, out, 
     _outputs(out, lse, B, Hq, D)
     _seqlens(seqlens, B)
     wp, wb = _ws(workspace)
-    fn = lib().fd_decode_paged
-    args = (B, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], q.data_ptr(), k_pages.data_ptr(),
-            v_pages.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), ctypes.c_float(scale), out.data_ptr(),
-            lse.data_ptr(), wp, wb, int(num_splits), _stream(stream, q.device))
-
-    def call():
-        rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, "fd_decode_paged")
-
-    return call
+    return _prepared("fd_decode_paged", (q, k_pages, v_pages, block_table, seqlens, out, lse, workspace), (
+        B, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], q.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), wp,
+        wb, int(num_splits), _stream(stream, q.device)))
 
 
 def prepare_decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_table, seqlens, scale, out, lse,
@@ -345,18 +368,12 @@ def prepare_decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, b
             raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor")
     _seqlens(seqlens, B)
     wp, wb = _ws(workspace)
-    fn = lib().fd_decode_quant_paged
-    args = (B, q_len, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], KV_CODES[kv_type], q.data_ptr(),
-            k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-            seqlens.data_ptr(), ctypes.c_float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, int(num_splits),
-            _stream(stream, q.device))
-
-    def call():
-        rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, "fd_decode_quant_paged")
-
-    return call
+    tensors = (q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
+    return _prepared("fd_decode_quant_paged", tensors, (
+        B, q_len, Hq, Hkv, D, page_size, num_pages, max_pages, LAYOUTS[layout], KV_CODES[kv_type], q.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+        seqlens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, int(num_splits),
+        _stream(stream, q.device)))
 
 
 def decode_quant_paged(q, k_pages, v_pages, k_scale, v_scale, kv_type, block_table, seqlens, scale, layout="HND",
@@ -420,15 +437,9 @@ def prepare_decode(q, k_cache, v_cache, seqlens, scale, out, lse, workspace=None
     _seqlens(seqlens, B)
     S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
     wp, wb = _ws(workspace)
-    fn = lib().fd_decode_splits
-    args = (B, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
-            ctypes.c_float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, S, _stream(stream, q.device))
-
-    def call():
-        rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, "fd_decode_splits")
-
+    call = _prepared("fd_decode_splits", (q, k_cache, v_cache, seqlens, out, lse, workspace), (
+        B, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(), float(scale),
+        out.data_ptr(), lse.data_ptr(), wp, wb, S, _stream(stream, q.device)))
     call.num_splits = S
     return call
 
@@ -449,15 +460,9 @@ def prepare_decode_multi(q, k_cache, v_cache, seqlens, scale, out, lse, workspac
     _seqlens(seqlens, B)
     S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
     wp, wb = _ws(workspace)
-    fn = lib().fd_decode_multi
-    args = (B, q_len, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
-            ctypes.c_float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, S, _stream(stream, q.device))
-
-    def call():
-        rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, "fd_decode_multi")
-
+    call = _prepared("fd_decode_multi", (q, k_cache, v_cache, seqlens, out, lse, workspace), (
+        B, q_len, Hq, Hkv, D, Lmax, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), seqlens.data_ptr(),
+        float(scale), out.data_ptr(), lse.data_ptr(), wp, wb, S, _stream(stream, q.device)))
     call.num_splits = S
     return call
 
@@ -501,16 +506,11 @@ def prepare_decode_quant(q, k_codes, v_codes, k_scale, v_scale, kv_type, seqlens
     _seqlens(seqlens, B)
     S = fd_plan(B, Hq, Hkv, D, Lmax) if num_splits is None else int(num_splits)
     wp, wb = _ws(workspace)
-    fn = lib().fd_decode_quant
-    args = (B, q_len, Hq, Hkv, D, Lmax, KV_CODES[kv_type], q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), seqlens.data_ptr(), ctypes.c_float(scale), out.data_ptr(),
-            lse.data_ptr(), wp, wb, S, _stream(stream, q.device))
-
-    def call():
-        rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, "fd_decode_quant")
-
+    tensors = (q, k_codes, v_codes, k_scale, v_scale, seqlens, out, lse, workspace)
+    call = _prepared("fd_decode_quant", tensors, (
+        B, q_len, Hq, Hkv, D, Lmax, KV_CODES[kv_type], q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(),
+        k_scale.data_ptr(), v_scale.data_ptr(), seqlens.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), wp, wb,
+        S, _stream(stream, q.device)))
     call.num_splits = S
     return call
 
@@ -605,36 +605,6 @@ FD_BLOCK_TOKENS = (16, 32, 64, 128)
 def _tensor(t, name, shape, dtype):
     if t.shape != shape or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {list(shape)}")
-
-
-def _one_device(*tensors):
-    """Index of the device that holds all of `tensors` (None entries aside)."""
-    devices = {t.device.index for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError("all tensors must be on one device")
-    return devices.pop()
-
-
-def _prepared(what, tensors, args):
-    """A no-argument callable that runs entry point `what` with `args`, with
-    the device of `tensors` as the current one. It holds the tensors (None
-    entries aside): their memory stays theirs as long as it lives."""
-    device = _one_device(*tensors)
-    fn = getattr(lib(), what)
-    # converted once here, not on every call
-    args = tuple(t(a) if a is not None else a for t, a in zip(fn.argtypes, args))
-
-    def call():
-        if torch.cuda.current_device() == device:
-            rc = fn(*args)
-        else:
-            with torch.cuda.device(device):
-                rc = fn(*args)
-        if rc != 0:
-            raise FdError(rc, what)
-
-    call.tensors = tensors
-    return call
 
 
 def _planned(device, B, Hq, Hkv, D, Lmax, num_splits):
