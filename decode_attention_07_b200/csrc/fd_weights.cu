@@ -229,6 +229,22 @@ int fd_decode_weights(int B, int q_len, int Hq, int Hkv, int D, int max_len, con
     pr.Hq = Hq;
     int sms;
     if ((rc = device_sms(&sms)) != FD_OK) return rc;
+    {   // what is written may not be what the kernels still read, nor one another
+        const size_t cache = static_cast<size_t>(B) * Hkv * max_len * D * 2, totals = cache / D * 2;
+        const size_t rows = static_cast<size_t>(B) * q_len * Hq;
+        const void *ins[4] = {q, k_cache, v_cache, seqlens};
+        const size_t in_n[4] = {rows * D * 2, cache, cache, static_cast<size_t>(B) * 4};
+        const void *outs[4] = {out, lse, workspace, weights_out};
+        const size_t out_n[4] = {rows * D * 4, rows * 4,
+                                 workspace ? head + fdh::workspace_bytes(B, Hq * q_len, Hkv, D, S) : 0, totals};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 4; ++j)
+                if (overlap(outs[i], out_n[i], ins[j], in_n[j])) return FD_ERR_OVERLAP;
+            for (int j = 0; j < i; ++j)
+                if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FD_ERR_OVERLAP;
+            if (i < 3 && weights_in && overlap(outs[i], out_n[i], weights_in, totals)) return FD_ERR_OVERLAP;
+        }
+    }
 
     CUtensorMap tk, tv;
     std::memset(&tk, 0, sizeof tk);

@@ -92,7 +92,8 @@ extern "C" {
 #define FD_ERR_BOUNDS       -13   /* debug builds only (-DFD_DEBUG): a device-side bounds check failed; the
                                      access was skipped and the call's outputs are invalid */
 
-#define FD_ERR_OVERLAP      -14   /* an output overlaps an input or another output (fd_decode_weights, fd_evict) */
+#define FD_ERR_OVERLAP      -14   /* an output (or the workspace) overlaps an input or another output: fd_evict, and
+                                     fd_decode_weights, which looks at all but the totals once it knows the device */
 
 #define FD_TILE_TOKENS     64     /* tokens per tile; split boundaries are multiples of this */
 #define FD_MAX_SPLITS      65535
@@ -317,8 +318,9 @@ FD_API int fd_decode_quant_block_paged(int B, int q_len, int Hq, int Hkv, int D,
  * half a step of the new scale. Every quotient rounds as the real number
  * does, ties included. New tokens must be finite, and the scale of a block
  * that holds older tokens finite and >= 0. Codes and scales of all other
- * positions and blocks are left as they were. One kernel on `stream`; no
- * workspace.
+ * positions and blocks are left as they were. What the call writes (the codes
+ * and scales of the touched blocks) may share no byte with what it reads, nor
+ * K's with V's; this is not checked. One kernel on `stream`; no workspace.
  * n_new = 0 or max_len = 0: nothing to do, no CUDA call. */
 FD_API int fd_quant_append(int B, int n_new, int Hkv, int D, int max_len, int block_tokens, int kv_type,
                            const uint16_t *k_new, const uint16_t *v_new, long long stride_b, long long stride_t,
@@ -343,8 +345,9 @@ FD_API int fd_quant_append_paged(int B, int n_new, int Hkv, int D, int page_size
  * seqlens[b]; later positions of weights_out are left as they were.
  * weights_in / weights_out: [B][Hkv][max_len] fp32, device, 4-byte aligned;
  * weights_in NULL counts as zeros, and may be weights_out itself (a total
- * kept in place) but not overlap it otherwise. out, lse: those of
- * fd_decode_multi. Two kernels on `stream`. Workspace:
+ * kept in place) but not overlap it otherwise (FD_ERR_OVERLAP, as for any
+ * other output or the workspace over an input or an output). out, lse: those
+ * of fd_decode_multi. Two kernels on `stream`. Workspace:
  * fd_weights_workspace_bytes(), of which 4 bytes per (cached position, column
  * of its kv head) hold logits; zero before its first use, as for fd_decode,
  * and again before it serves another shape. */
