@@ -127,7 +127,7 @@ struct QuantConsumer {
         }
     }
 
-    // A token of the row (unsigned: a tile or two past a row of nearly 2^31 tokens).
+    // A token of the row (tokens ahead are counted unsigned: a tile or two past a row of nearly 2^31 tokens).
     __device__ __forceinline__ int clip(uint32_t t) const { return static_cast<int>(min(t, static_cast<uint32_t>(last))); }
 
     // Pages of the slice's 16-token blocks from token t0 on (past the row: of its last token).
@@ -167,11 +167,11 @@ struct QuantConsumer {
         }
     }
 
-    static constexpr int kStride = kConsumerWarps * kTok;   // tokens from one tile of a group to its next
+    static constexpr uint32_t kStride = kConsumerWarps * kTok;   // tokens from one tile of a group to its next
 
     // Segment start: the scales of the group's first tile (t0: first token of
     // this warp's slice in it).
-    __device__ __forceinline__ void start_segment(const SplitParams &p, const Cursor &c, int t0, int, int L) {
+    __device__ __forceinline__ void start_segment(const SplitParams &p, const Cursor &c, uint32_t t0, int L) {
         last = L - 1;
         const size_t row = kPagedScales ? static_cast<size_t>(c.h) : static_cast<size_t>(c.b) * p.Hkv + c.h;
         kp = p.k_scale + row * p.blocks;
@@ -188,7 +188,7 @@ struct QuantConsumer {
 
     // Before a tile: its scales have been asked for a tile ago; ask for those
     // of the group's next one.
-    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &, int t0, int, int) {
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &, uint32_t t0) {
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {   // (copied here, not where they are asked for: a copy waits for its load)
             const bool first = mb > 0 && p.blk_shift > 4;

@@ -552,9 +552,9 @@ struct GroupConsumer {
 
     __device__ __forceinline__ void set_row(const SplitParams &, int) {}   // bf16 cache: no per-head scales
 
-    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int, int) {}
+    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int) {}
     // Before the tile of row tokens [t0, t0 + 16) of this warp: where its logits go.
-    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0, int, int) {
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0) {
         lcols = logit_cols(p.cols);
         lg = p.logits + ((static_cast<size_t>(c.b) * p.Hkv + c.h) * p.Lmax + t0) * lcols;
     }
@@ -767,8 +767,8 @@ struct HeadConsumer {
 
     __device__ __forceinline__ void init(const SplitParams &) {}   // one query, one head: no offsets
     __device__ __forceinline__ void set_row(const SplitParams &, int) {}
-    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int, int) {}
-    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0, int, int) {
+    __device__ __forceinline__ void start_segment(const SplitParams &, const Cursor &, int, int) {}
+    __device__ __forceinline__ void before_tile(const SplitParams &p, const Cursor &c, int t0) {
         lg = p.logits + (static_cast<size_t>(c.b) * p.Hkv + c.h) * p.Lmax + t0;
     }
 
@@ -1366,16 +1366,14 @@ __global__ void __launch_bounds__(split_threads<kPaged>(), 1)
             cons.set_row(p, c.h);
             if constexpr (Consumer::kTileHook) {   // first tile of this group in the segment
                 const int k0 = (group - static_cast<int>(seq % kGroupsC) + kGroupsC) % kGroupsC;
-                if (k0 < seg) cons.start_segment(p, c, (c.tile + k0) * kTileTokens + kTok * slice, slice, L);
+                if (k0 < seg) cons.start_segment(p, c, (c.tile + k0) * kTileTokens + kTok * slice, L);
             }
             for (int k = 0; k < seg; ++k, ++seq) {
                 if (static_cast<int>(seq % kGroupsC) != group) continue;
                 const int stage = static_cast<int>(seq % kStages);
                 const uint32_t phase = (seq / kStages) & 1u;
-                if constexpr (Consumer::kTileHook) {   // first token of this warp's slice; the same in the group's next tile
-                    const int t0 = (c.tile + k) * kTileTokens + kTok * slice;
-                    cons.before_tile(p, c, t0, k + kGroupsC < seg ? t0 + kGroupsC * kTileTokens : -1, L);
-                }
+                if constexpr (Consumer::kTileHook)   // with the first token of this warp's slice
+                    cons.before_tile(p, c, (c.tile + k) * kTileTokens + kTok * slice);
                 wait_bounded(&full[stage], phase, abort);   // on abort: keep going, outputs are flagged invalid
                 const uint8_t *st = ring + stage * Cfg::kStageBytes;
                 if (k < kGroupsC) cons.load_q(st + 2 * Cfg::kTileBytes, p.cols);
