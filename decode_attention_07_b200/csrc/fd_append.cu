@@ -326,7 +326,7 @@ int append(int B, int n_new, int Hkv, int D, int max_len, int block_tokens, int 
     p.Hkv = Hkv;
     p.max_len = max_len;
     p.touched = static_cast<int>((static_cast<long long>(n_new) + block_tokens - 2) / block_tokens + 1);
-    p.blocks = ((pl ? pl->page_size : max_len) + block_tokens - 1) / block_tokens;
+    p.blocks = static_cast<int>(((pl ? pl->page_size : max_len) + block_tokens - 1LL) / block_tokens);
     if (pl) {
         p.block_table = pl->block_table;
         p.max_pages = pl->max_pages;

@@ -46,7 +46,7 @@ int run_block(const Problem &pr, int q_len, int kv_type, int block_tokens, const
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     while ((1 << p.blk_shift) < block_tokens) ++p.blk_shift;
-    p.blocks = ((pl ? pl->page_size : pr.max_len) + block_tokens - 1) / block_tokens;
+    p.blocks = static_cast<int>(((pl ? pl->page_size : pr.max_len) + block_tokens - 1LL) / block_tokens);
     CUtensorMap tk, tv, rk, rv;
     std::memset(&tk, 0, sizeof tk);
     std::memset(&tv, 0, sizeof tv);

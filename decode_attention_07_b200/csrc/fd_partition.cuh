@@ -47,7 +47,10 @@ __host__ __device__ __forceinline__ int clamp_len(int L, int Lmax) {
     return L < 0 ? 0 : (L > Lmax ? Lmax : L);
 }
 
-__host__ __device__ __forceinline__ int tiles_of(int L) { return (L + kTileTokens - 1) / kTileTokens; }
+// L >= 0 (unsigned: L + 63 may pass 2^31).
+__host__ __device__ __forceinline__ int tiles_of(int L) {
+    return static_cast<int>((static_cast<unsigned>(L) + kTileTokens - 1) / kTileTokens);
+}
 
 // First flat tile of run i (i in [0, P]).
 __host__ __device__ __forceinline__ long long run_begin(long long i, long long N, long long P) {

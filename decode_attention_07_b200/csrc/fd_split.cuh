@@ -283,10 +283,10 @@ __device__ __forceinline__ void drain_copies(uint64_t *full, uint32_t issued, ui
 // row is touched).
 template <int kRowBytes>
 __device__ __forceinline__ void prefetch_row_span(const SplitParams &p, int z, int t0, int t1) {
-    const int tok0 = t0 * kTileTokens, tok1 = min(t1 * kTileTokens, p.Lmax);
-    if (tok1 <= tok0) return;
+    const int tok0 = t0 * kTileTokens, tokens = min((t1 - t0) * kTileTokens, p.Lmax - tok0);
+    if (tokens <= 0) return;
     const size_t off = (static_cast<size_t>(z) * p.Lmax + tok0) * kRowBytes;
-    const uint32_t bytes = static_cast<uint32_t>(tok1 - tok0) * kRowBytes;
+    const uint32_t bytes = static_cast<uint32_t>(tokens) * kRowBytes;
     bulk_prefetch_l2(static_cast<const uint8_t *>(p.k_base) + off, bytes);
     bulk_prefetch_l2(static_cast<const uint8_t *>(p.v_base) + off, bytes);
 }
