@@ -163,8 +163,8 @@ def _outputs(out, lse, B, Hq, D):
 
 
 def _seqlens(seqlens, B):
-    if seqlens.shape != (B,) or seqlens.dtype != torch.int32 or not seqlens.is_cuda:
-        raise ValueError("seqlens must be an int32 CUDA tensor of shape [B]")
+    if seqlens.shape != (B,) or seqlens.dtype != torch.int32 or not seqlens.is_cuda or not seqlens.is_contiguous():
+        raise ValueError("seqlens must be a contiguous int32 CUDA tensor of shape [B]")
 
 
 def _ws(workspace):

@@ -89,3 +89,29 @@ def test_errors_are_raised_by_the_call(kind):
     with pytest.raises(fd.FdError) as e:
         call()
     assert e.value.code == -6
+
+
+@pytest.mark.parametrize("kind", list(PREPARE))
+def test_lengths_with_gaps_are_refused(kind):
+    """A view's lengths are not side by side in memory, where the kernels read them."""
+    args, rest = arguments(kind)
+    at = next(i for i, a in enumerate(args) if isinstance(a, torch.Tensor) and a.dtype == torch.int32 and a.dim() == 1)
+    spaced = torch.tensor([L, 1, 99, 1], dtype=torch.int32, device="cuda")
+    for bad in (spaced[::2], args[at][:1].expand(B)):
+        with pytest.raises(ValueError):
+            PREPARE[kind](*args[:at], bad, *args[at + 1:], *rest)
+    PREPARE[kind](*args[:at], spaced[::2].contiguous(), *args[at + 1:], *rest)()
+    torch.cuda.synchronize()
+
+
+def test_lengths_with_gaps_are_refused_by_the_direct_calls():
+    (q, k, v, lens, scale, out, lse, ws), _ = arguments("decode")
+    bad = torch.tensor([L, 1, 99, 1], dtype=torch.int32, device="cuda")[::2]
+    for call in (lambda n: fd.fd_decode(q, k, v, n, scale, out, lse, ws), lambda n: fd.decode(q, k, v, n, scale),
+                 lambda n: fd.fd_decode_splits(q, k, v, n, scale, out, lse, ws, S),
+                 lambda n: fd.fd_split(q, k, v, n, scale, out, lse, ws, S),
+                 lambda n: fd.fd_combine(B, G * HKV, HKV, D, L, n, out, lse, ws, S),
+                 lambda n: fd.fd_decode_static(q, k, v, n, scale, out, lse)):
+        with pytest.raises(ValueError):
+            call(bad)
+    torch.cuda.synchronize()
