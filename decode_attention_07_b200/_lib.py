@@ -427,6 +427,9 @@ def fd_version() -> int:
 
 
 # ------------------------------------------------------------ convenience --
+# Prepared calls, and calls that allocate their outputs and workspace: these
+# allocate on the stream they run on, and their results may be used and dropped
+# on the stream that was current, once that has waited for the call.
 
 def prepare_decode(q, k_cache, v_cache, seqlens, scale, out, lse, workspace=None, num_splits=None, stream=None):
     """Check and marshal the arguments once; return a no-argument callable

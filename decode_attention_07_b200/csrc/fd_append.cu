@@ -25,7 +25,7 @@
 // token or two, the launch and two dependent loads (length, then data).
 // 16384 tokens of 32 heads (403 MB): 68 us in short bursts (5.9 TB/s), 75 us
 // sustained; 16 uneven chunks of 1000 tokens into pages (72 MB): 15.9 us; one
-// token for each of 64 sequences: 5.2 us. Wider groups (4 loads a thread) and
+// token for each of 64 sequences: 5.3 us in bursts, 5.8 sustained. Wider groups (4 loads a thread) and
 // several blocks of tokens in turn per thread block measured slower: what
 // counts is loads in flight, 8 a thread at 1024 threads a SM.
 // A group of 1 to 8 warps per (block of tokens, kv head, K or V), 8 loads of

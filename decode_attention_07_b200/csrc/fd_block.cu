@@ -4,10 +4,10 @@
 //
 // What bounds it: the cache's codes, 2 D bytes per (token, kv head) plus
 // 8 / T bytes of scales, each read once. One sequence of 16384 E4M3 tokens, 32
-// heads (134 MB): 27.4 us, 4.9 TB/s; 131072 int8 tokens, 64 / 8 heads (269 MB):
-// 52 us in short bursts (5.1 TB/s), 57 us sustained, where the consumers'
+// heads (134 MB): 27.3 us, 4.9 TB/s; 131072 int8 tokens, 64 / 8 heads (269 MB):
+// 52 us in short bursts (5.1 TB/s), 56.5 us sustained, where the consumers'
 // arithmetic takes over from memory; 32 uneven sequences in 64-token pages
-// (268 MB): 58 us, 12 of them waiting for the block that holds the most short
+// (268 MB): 58 to 61 us, 12 of them waiting for the block that holds the most short
 // rows.
 #include "fd_host.cuh"
 #include "fd_quant.cuh"

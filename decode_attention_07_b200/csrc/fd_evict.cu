@@ -26,7 +26,10 @@
 // before the first copy can start. 8 rows of 131072 tokens cut to 32768
 // (275 MB): 64 us, of which the copy 42 (6.4 TB/s, a copy's rate) and the
 // selection 20 (2.6 a pass, 0.8 of it the cluster barrier); 512 rows of up to
-// 4096 cut to 1000 (474 MB): 89 us. Clusters of 16 blocks (of 512 threads)
+// 4096 cut to 1000 (474 MB): 89 us. Slices past the registers (rows of more than
+// 131072 tokens, or fewer blocks a row) are read again in each pass: 8 rows of
+// 262144 cut to 65536 take 130 us, 32 rows of 131072 cut to 32768 211, and one
+// row of a million cut to 100000, which eight blocks select, 159. Clusters of 16 blocks (of 512 threads)
 // were no faster: their barrier and remote reads grow as their slices shrink.
 #include <cooperative_groups.h>
 

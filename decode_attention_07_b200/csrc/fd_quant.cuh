@@ -62,9 +62,11 @@
 //     scheduler; 12 or 16 consumer warps of 16 tokens each were slower, 60 and
 //     61 us against 54 on 64 heads over 131072 int8 tokens), so the arithmetic
 //     counts: p = 2^(fma(q.k, c, kPScale - m)) and one factor per (block,
-//     column) for the values; the test for a new reference looks at the p
-//     themselves. 32 heads over 16384 E4M3 tokens: 27.2 us (one scale per
-//     head 25.8); 64/8 heads over 131072 int8 tokens: 52.3 us (48.6).
+//     column) for the values; the test for a new m or r looks at the p and
+//     p r v_scale themselves. In short bursts (20 calls a graph, the figures
+//     above too), 32 heads over 16384 E4M3 tokens: 27.2 us (one scale per head
+//     25.8); 64/8 heads over 131072 int8 tokens: 52.2 us (48.6). Called without
+//     a pause the chip's clock falls and the latter takes 56.5 us.
 //   * A warp reads its 16-token blocks' scales (through the block table for
 //     paged caches) one tile of its group ahead, with loads from L2, so their
 //     latency lies behind a tile's arithmetic.

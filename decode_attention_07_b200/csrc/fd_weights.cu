@@ -15,9 +15,9 @@
 // What bounds it: 4 D bytes of K and V and 8 bytes of totals per (token, kv
 // head); the logits' round trip is 8 bytes a column, mostly through L2. One
 // sequence of 16384 tokens, 32 heads (273 MB): 46 us, 5.9 TB/s (attention
-// alone 41); 131072 tokens, 64 / 8 heads (545 MB): 96 us (80); the second
-// kernel adds a launch and two dependent loads, 4 to 6 us, which is most of a
-// small call.
+// alone 41); 131072 tokens, 64 / 8 heads (545 MB): 96 us in short bursts (80),
+// 98 sustained; the second kernel adds a launch and two dependent loads, 4 to
+// 6 us, which is most of a small call.
 #include "fd_host.cuh"
 
 namespace fd {

@@ -58,7 +58,8 @@
  * asynchronous on `stream` (a cudaStream_t; NULL = legacy default stream)
  * and never synchronise, except fd_device_status. Every entry point returns
  * FD_OK (0) or a negative FD_ERR_* code; argument checks run before any CUDA
- * call, so a rejected call launches nothing.
+ * call (part of FD_ERR_OVERLAP's after the device is known), so a rejected
+ * call launches nothing.
  */
 #ifndef FD_H_
 #define FD_H_
