@@ -56,7 +56,7 @@
 //     r is chosen like m, by the same rare branch, to keep the column's largest
 //     contribution p r v_scale in f16's range: P keeps its bits relative to
 //     the row's largest contribution, not to its largest scale or weight. r is
-//     at most 2^126: a column that has met only zero scales, however heavy,
+//     at most 2^119: a column that has met only zero scales, however heavy,
 //     has a finite r, and zero weights times it are zero.
 //   * Consumers are what bounds it next to memory (two consumer warps per
 //     scheduler; 12 or 16 consumer warps of 16 tokens each were slower, 60 and
@@ -524,7 +524,8 @@ struct QuantConsumer {
     // m is a whole number, so that r and the references' differences are
     // exact. s: the tile's products q . k.
     static constexpr float kNoRef = -3e38f;
-    static constexpr float kMaxLog2R = 126.f;     // below it, an output's contribution is no normal float
+    static constexpr float kMaxLog2R = 119.f;     // an output of 2^-126 then still has P at 1, a normal f16
+    static constexpr float kMinLog2R = -126.f;    // a scale of nearly 2^128 then has P below 2^10
     static constexpr float kMaxF = 8.507059e37f;  // 2^126
     // 2^e of whole e in [-126, 126], and back.
     static __device__ __forceinline__ float exp2i(float e) {
@@ -536,7 +537,7 @@ struct QuantConsumer {
     __device__ __forceinline__ void softmax_block(float (&s)[MB][NT][4], bool ends, int valid,
                                                   uint32_t (&bh)[MB][NT][2], uint32_t (&bl)[MB][NT][2]) {
         constexpr float kMost = 32768.f;   // 2^(kLazy + kPScale)
-        static_assert(kLazy + kPScale == 15.f, "kMost");
+        static_assert(kLazy + kPScale == 15.f && kPScale == 7.f, "kMost, and the factor that to_smem takes off");
         float p[MB][NT][4], f[MB][NT][2];
         float most = 0.f;
         auto weights = [&] {
@@ -586,7 +587,7 @@ struct QuantConsumer {
                     const float dm = m[nt][e] - xm;
                     // relative to the new m: the largest contribution that r stood for so far, and the tile's
                     const float was = dm - log2i(r[nt][e]);
-                    const float y = fminf(fmaxf(fmaxf(ceilf(ym - xm), was), -kMaxLog2R), kMaxLog2R);
+                    const float y = fminf(fmaxf(fmaxf(ceilf(ym - xm), was), -kMaxLog2R), -kMinLog2R);
                     const float alpha = ex2(was - y);
                     l[nt][e] *= ex2(dm);
 #pragma unroll
@@ -611,8 +612,8 @@ struct QuantConsumer {
     }
 
     // This warp's (o, m, l) into a merge buffer slot: o[G][D] with the head
-    // dims back in order and the value scale applied, then m[G] (base 2,
-    // without the 2^kPScale factor), l[G].
+    // dims back in order and the value scale applied, then m[G] (base 2, with
+    // the 2^kPScale factor of o and l taken off), l[G].
     __device__ __forceinline__ void to_smem(float *wb) {
         constexpr int S = merge_head_stride<D>();
         const int lane = threadIdx.x & 31;
@@ -626,9 +627,13 @@ struct QuantConsumer {
                 for (int sh = 4; sh < 32; sh <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
             const int ha = nt * 8 + 2 * cc, hb = ha + 1;
             float va = vmul, vb = vmul;
-            if constexpr (kBlock) {   // without r, and the merge's "no token" for a column without
-                va = exp2i(-log2i(r[nt][0]));
-                vb = exp2i(-log2i(r[nt][1]));
+            if constexpr (kBlock) {
+                // without r and 2^kPScale (taken off the sum, not off m: the hardware log2's error grows with
+                // the sum's distance from 1), and the merge's "no token" for a column without
+                va = exp2i(-log2i(r[nt][0]) - kPScale);
+                vb = exp2i(-log2i(r[nt][1]) - kPScale);
+                l[nt][0] *= 1.f / 128.f;
+                l[nt][1] *= 1.f / 128.f;
                 if (m[nt][0] == kNoRef) m[nt][0] = -INFINITY;
                 if (m[nt][1] == kNoRef) m[nt][1] = -INFINITY;
             }
@@ -641,8 +646,9 @@ struct QuantConsumer {
                 *reinterpret_cast<float2 *>(wb + hb * S + d0) = make_float2(o[nt][c][1] * vb, o[nt][c][3] * vb);
             }
             if (r0 == 0) {
-                wb[G * S + ha] = m[nt][0] == -INFINITY ? -INFINITY : m[nt][0] - kPScale;
-                wb[G * S + hb] = m[nt][1] == -INFINITY ? -INFINITY : m[nt][1] - kPScale;
+                constexpr float off = kBlock ? 0.f : kPScale;
+                wb[G * S + ha] = m[nt][0] == -INFINITY ? -INFINITY : m[nt][0] - off;
+                wb[G * S + hb] = m[nt][1] == -INFINITY ? -INFINITY : m[nt][1] - off;
                 wb[G * S + G + ha] = l[nt][0];
                 wb[G * S + G + hb] = l[nt][1];
             }

@@ -116,3 +116,24 @@ def test_values_scaled_by_a_power_of_two(kv, g, power):
     assert torch.equal(la, lb)
     err = ((b.double() - want).abs() / want.abs()).max()
     assert err <= 2 * 2.0 ** -22 + 2.0 ** -24, f"relative difference {err:.3e}"
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("g", [4, 16])
+def test_the_log_sum_exp_of_one_token_is_its_logit(kv, g):
+    """One-hot queries, so the products are exact. What is left: four roundings
+    of the logit and its base-2 form, the argument of the exponential (below 8
+    in size, 2^-21), the exponential (2^-22 of it) and the logarithm of a number
+    within a factor of 2 of 1 (2^-22), in base 2: below 2^-20 ln 2, and 2^-22 of
+    the logit."""
+    B, Hkv, D, T = 64, 2, 64, 16
+    k8, v8, ks, vs = make(B, Hkv, 1, D, T, kv, [1] * B, 57)
+    q = torch.zeros((B, g * Hkv, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 5] = query(B, 1, g * Hkv, 1, 58)[..., 0]
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    out, lse = fd.decode_quant_block(q, k8, v8, ks, vs, kv, T, lens, 0.125, num_splits=1)
+    torch.cuda.synchronize()
+    k = dense(k8, ks, T, kv, [1] * B)
+    z = torch.einsum("bhgd,bhd->bhg", q.double().view(B, Hkv, g, D), k[:, :, 0]).reshape(B, g * Hkv) * 0.125
+    err = (lse.double() - z).abs()
+    assert (err <= 0.7 * 2.0 ** -20 + 2.0 ** -22 * z.abs()).all(), f"off by {float(err.max()):.2e}"
